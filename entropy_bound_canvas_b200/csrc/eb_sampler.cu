@@ -19,16 +19,17 @@
 #include <mutex>
 #include <new>
 
-#include <cudaTypedefs.h>
-
 #include "eb_finish.cuh"
+#include "eb_host.cuh"
 #include "eb_lmhead.cuh"
 #include "eb_stream.cuh"
 
 namespace {
 
+using ebk::DeviceGuard;
 using ebk::Rec;
 using ebk::StepArgs;
+using ebk::align256;
 
 struct KernelCfg {
   const void* fn = nullptr;
@@ -127,20 +128,6 @@ struct eb_sampler {
 };
 
 namespace {
-
-// Restores the caller's current device on scope exit.
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = false;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) ok = true;
-  }
-  ~DeviceGuard() {
-    if (prev >= 0) cudaSetDevice(prev);
-  }
-};
-
-size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 int validate_config(const eb_config_t* c) {
   if (!c) return EB_ERR_INVALID_ARG;
@@ -423,39 +410,8 @@ bool is_slice(const eb_sampler* h) {
 }
 
 // ---------------------------------------------------------------------------
-// LM-head step: tensor maps and launch
+// LM-head step: launch
 // ---------------------------------------------------------------------------
-PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    cudaGetLastError();
-  });
-  return fn;
-}
-
-// A bf16 matrix [outer][inner] (inner contiguous), read in boxes of
-// box_outer x 64 with the 128-byte swizzle the MMA descriptors expect.
-bool make_tmap(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
-               uint32_t box_outer) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tmap_encoder();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {inner * 2};
-  cuuint32_t box[2] = {(cuuint32_t)ebk::kLmBK, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-         CUDA_SUCCESS;
-}
-
 // Sizes the LM-head kernels accept: the hidden size a multiple of 64, the
 // vocabulary a multiple of 256 (one MMA N tile), 16-byte aligned operands.
 int lm_check(const void* hidden, const void* weight, int64_t rows, int64_t V, int64_t d) {
@@ -477,8 +433,8 @@ int lm_split_count(int sms, int64_t rows, int64_t V) {
 int lm_launch(bool sampler, const DeviceAttrs& d, const void* hidden, const void* weight,
               ebk::LmArgs& p, cudaStream_t st) {
   CUtensorMap th, tw;
-  if (!make_tmap(&th, hidden, (uint64_t)p.d, (uint64_t)p.rows, ebk::kLmBM) ||
-      !make_tmap(&tw, weight, (uint64_t)p.d, (uint64_t)p.V, ebk::kLmBN))
+  if (!ebk::make_tmap(&th, hidden, (uint64_t)p.d, (uint64_t)p.rows, ebk::kLmBK, ebk::kLmBM) ||
+      !ebk::make_tmap(&tw, weight, (uint64_t)p.d, (uint64_t)p.V, ebk::kLmBK, ebk::kLmBN))
     return EB_ERR_CUDA;
   const size_t smem = ebk::lm_layout(sampler).total;
   if (smem > d.optin) return EB_ERR_UNSUPPORTED;
