@@ -19,6 +19,7 @@ from __future__ import annotations
 import ctypes as C
 import dataclasses
 import os
+from typing import Any, NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libebsampler.so")
@@ -26,7 +27,7 @@ LIB_PATH = os.path.join(_HERE, "libebsampler.so")
 F32, BF16 = 0, 1
 RULE_ENTROPY_BOUND, RULE_BLOCK_REFINEMENT, RULE_ENTROPY_BOUND_MI = 0, 1, 2
 STOP_ACTIVE, STOP_ADAPTIVE, STOP_ALL_COMMITTED, STOP_LAST_STEP = 0, 1, 2, 3
-STATUS_BAD_TOKEN, STATUS_NONFINITE, STATUS_TIMEOUT = 1, 2, 4
+STATUS_BAD_TOKEN, STATUS_NONFINITE, STATUS_TIMEOUT, STATUS_BAD_OFFSETS = 1, 2, 4, 8
 GUMBEL_GROUP = 64
 
 EB_OK = 0
@@ -54,6 +55,53 @@ class Config(C.Structure):
         ("canvas_offset", C.c_int32), ("seed", C.c_uint64),
         ("editing_threshold", C.c_double), ("vocab_offset", C.c_int32), ("vocab_total", C.c_int32),
     ]
+
+
+class ScoreInput(C.Structure):
+    """eb_score_input_t."""
+    _fields_ = [
+        ("logits", C.c_void_p), ("dtype", C.c_int32), ("rows", C.c_int32), ("V", C.c_int32),
+        ("ld", C.c_int64), ("tokens", C.c_void_p), ("temperatures", C.c_void_p),
+        ("temperature", C.c_double),
+    ]
+
+
+class Policy(C.Structure):
+    """eb_policy_t."""
+    _fields_ = [
+        ("old_logprobs", C.c_void_p), ("advantages", C.c_void_p), ("ref_logprobs", C.c_void_p),
+        ("weights", C.c_void_p), ("clip_low", C.c_double), ("clip_high", C.c_double),
+        ("kl_coef", C.c_double), ("entropy_coef", C.c_double), ("scale", C.c_double),
+    ]
+
+
+class Preference(C.Structure):
+    """eb_preference_t."""
+    _fields_ = [
+        ("offsets", C.c_void_p), ("pairs", C.c_int32), ("ref_logprobs", C.c_void_p),
+        ("beta", C.c_double), ("label_smoothing", C.c_double), ("margin", C.c_double),
+        ("average", C.c_int32), ("scale", C.c_double),
+    ]
+
+
+class TokenScores(NamedTuple):
+    logprobs: Any        # [rows] fp32
+    entropies: Any       # [rows] fp32, or None
+
+
+class PolicyLoss(NamedTuple):
+    terms: Any           # [5] fp32: loss, policy term, KL, entropy, clipped share
+    logprobs: Any        # [rows] fp32
+    entropies: Any       # [rows] fp32
+    d_logits: Any        # as the logits, or None
+
+
+class PreferenceLoss(NamedTuple):
+    loss: Any               # [1] fp32
+    losses: Any             # [pairs] fp32
+    sequence_logprobs: Any  # [2 pairs] fp32
+    logprobs: Any           # [rows] fp32
+    d_logits: Any           # as the logits, or None
 
 
 _LIB = None
@@ -108,6 +156,28 @@ def _lib():
         L.eb_lmhead_reserve.restype = i32
         L.eb_lmhead_step.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp]
         L.eb_lmhead_step.restype = i32
+        sip, i64, dbl = C.POINTER(ScoreInput), C.c_int64, C.c_double
+        L.eb_scorer_init.argtypes = [C.POINTER(vp), C.c_int32, i32]
+        L.eb_scorer_init.restype = i32
+        L.eb_token_logprobs.argtypes = [vp, sip, vp, vp, vp]
+        L.eb_token_logprobs.restype = i32
+        L.eb_token_logprobs_backward.argtypes = [vp, sip, vp, vp, vp, i64, vp]
+        L.eb_token_logprobs_backward.restype = i32
+        L.eb_policy_loss.argtypes = [vp, sip, C.POINTER(Policy), vp, vp, vp, vp, i64, vp]
+        L.eb_policy_loss.restype = i32
+        L.eb_preference_loss.argtypes = [vp, sip, C.POINTER(Preference), vp, vp, vp, vp, vp, i64,
+                                         vp]
+        L.eb_preference_loss.restype = i32
+        L.eb_lmhead_logprobs.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, dbl, vp, vp, vp]
+        L.eb_lmhead_logprobs.restype = i32
+        L.eb_scorer_status.argtypes = [vp, u32p, i32, vp]
+        L.eb_scorer_status.restype = i32
+        L.eb_scorer_set_wait_limit.argtypes = [vp, C.c_uint64]
+        L.eb_scorer_set_wait_limit.restype = i32
+        L.eb_scorer_workspace_bytes.argtypes = [vp]
+        L.eb_scorer_workspace_bytes.restype = C.c_size_t
+        L.eb_scorer_destroy.argtypes = [vp]
+        L.eb_scorer_destroy.restype = None
         _LIB = L
     return _LIB
 
@@ -407,6 +477,227 @@ class EBSampler:
     def close(self):
         if getattr(self, "_h", None):
             _lib().eb_sampler_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+class EBScorer:
+    """Scores sampled tokens and learns from them, on one CUDA device: token
+    log-probabilities and entropies with their gradient, the clipped policy
+    loss and the preference loss with theirs (eb_scorer_t of
+    include/eb_sampler.h, which gives the formulas).
+
+    A row is one position.  Logits are [rows, V] with unit stride along V (a
+    [B, L, V] tensor is taken as B*L rows), fp32 or bf16; tokens int32, a
+    negative one ignores its row; temperature a number or an fp32 tensor of
+    one per row.  Results are allocated here unless ``out`` gives the
+    gradient's buffer, which may be the logits themselves.  Calls run on the
+    device's current stream, never synchronise, and can be captured in a CUDA
+    graph; one scorer per stream at a time.
+    """
+
+    def __init__(self, max_rows: int, device=None):
+        torch = _torch()
+        self.device = torch.device("cuda", torch.cuda.current_device() if device is None
+                                   else torch.device(device).index or 0)
+        self.max_rows = int(max_rows)
+        h = C.c_void_p()
+        _check(_lib().eb_scorer_init(C.byref(h), self.max_rows, self.device.index),
+               "eb_scorer_init")
+        self._h = h
+
+    # -- helpers --------------------------------------------------------------
+    def _stream(self):
+        return _torch().cuda.current_stream(self.device).cuda_stream
+
+    def _vector(self, t, n, dtype, name):
+        """Address of a contiguous tensor of n values (None: a null pointer)."""
+        if t is None:
+            return None
+        if not isinstance(t, _torch().Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, scorer is on {self.device}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous and hold {n} values, "
+                             f"got {tuple(t.shape)}")
+        return t.data_ptr()
+
+    def _matrix(self, t, name):
+        """(2-D view [rows, V], elements between rows) of logits or a gradient."""
+        torch = _torch()
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if t.dtype != torch.float32 and t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be float32 or bfloat16")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, scorer is on {self.device}")
+        if t.dim() < 2:
+            raise ValueError(f"{name} must be [rows, V]")
+        if t.dim() > 2:
+            try:
+                t = t.view(-1, t.shape[-1])
+            except RuntimeError:
+                raise ValueError(f"{name}: the rows must lie at one stride") from None
+        rows, V = t.shape
+        if V > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have unit stride along V")
+        ld = t.stride(0) if rows > 1 else V
+        if ld < V:
+            raise ValueError(f"{name}: rows overlap")
+        return t, ld
+
+    def _input(self, logits, tokens, temperature):
+        torch = _torch()
+        z, ld = self._matrix(logits, "logits")
+        rows, V = z.shape
+        s = ScoreInput()
+        s.logits = z.data_ptr()
+        s.dtype = F32 if z.dtype == torch.float32 else BF16
+        s.rows, s.V, s.ld = rows, V, ld
+        s.tokens = self._vector(tokens, rows, torch.int32, "tokens")
+        if isinstance(temperature, torch.Tensor):
+            s.temperatures = self._vector(temperature, rows, torch.float32, "temperature")
+        else:
+            s.temperature = float(temperature)
+        return s
+
+    def _gradient(self, logits, out):
+        """(gradient tensor shaped as the logits, its address, its row stride)."""
+        torch = _torch()
+        if out is None:
+            out = torch.empty(logits.shape, dtype=logits.dtype, device=self.device)
+        elif out.shape != logits.shape or out.dtype != logits.dtype:
+            raise ValueError("out must have the logits' shape and type")
+        d, ldd = self._matrix(out, "out")
+        return out, d.data_ptr(), ldd
+
+    def _new(self, n):
+        torch = _torch()
+        return torch.empty((n,), dtype=torch.float32, device=self.device)
+
+    # -- calls ------------------------------------------------------------------
+    def token_logprobs(self, logits, tokens, temperature=1.0, entropies: bool = True):
+        """Each row's log p[token] and (unless entropies=False) entropy."""
+        s = self._input(logits, tokens, temperature)
+        lp = self._new(s.rows)
+        h = self._new(s.rows) if entropies else None
+        _check(_lib().eb_token_logprobs(self._h, C.byref(s), lp.data_ptr(),
+                                        h.data_ptr() if entropies else None, self._stream()),
+               "eb_token_logprobs")
+        return TokenScores(lp, h)
+
+    def token_logprobs_backward(self, logits, tokens, d_logprobs, d_entropies=None,
+                                temperature=1.0, out=None):
+        """The gradient for the logits from those of token_logprobs' results."""
+        torch = _torch()
+        s = self._input(logits, tokens, temperature)
+        out, ptr, ldd = self._gradient(logits, out)
+        _check(_lib().eb_token_logprobs_backward(
+            self._h, C.byref(s), self._vector(d_logprobs, s.rows, torch.float32, "d_logprobs"),
+            self._vector(d_entropies, s.rows, torch.float32, "d_entropies"), ptr, ldd,
+            self._stream()), "eb_token_logprobs_backward")
+        return out
+
+    def policy_loss(self, logits, tokens, old_logprobs, advantages, ref_logprobs=None,
+                    weights=None, temperature=1.0, clip_low=0.2, clip_high=0.2, kl_coef=0.0,
+                    entropy_coef=0.0, scale=1.0, grad: bool = True, out=None):
+        """Clipped policy loss with a KL term and an entropy bonus, and its
+        gradient for the logits (grad=False: the loss alone)."""
+        f32 = _torch().float32
+        s = self._input(logits, tokens, temperature)
+        n = s.rows
+        p = Policy(self._vector(old_logprobs, n, f32, "old_logprobs"),
+                   self._vector(advantages, n, f32, "advantages"),
+                   self._vector(ref_logprobs, n, f32, "ref_logprobs"),
+                   self._vector(weights, n, f32, "weights"), clip_low, clip_high, kl_coef,
+                   entropy_coef, scale)
+        d, ptr, ldd = self._gradient(logits, out) if grad else (None, None, 0)
+        terms, lp, h = self._new(5), self._new(n), self._new(n)
+        _check(_lib().eb_policy_loss(self._h, C.byref(s), C.byref(p), terms.data_ptr(),
+                                     lp.data_ptr(), h.data_ptr(), ptr, ldd, self._stream()),
+               "eb_policy_loss")
+        return PolicyLoss(terms, lp, h, d)
+
+    def preference_loss(self, logits, tokens, offsets, ref_logprobs=None, beta=0.1,
+                        label_smoothing=0.0, margin=0.0, average: bool = False, temperature=1.0,
+                        scale=1.0, grad: bool = True, out=None):
+        """Preference loss over pairs of sequences and its gradient for the
+        logits.  offsets [2 pairs + 1] int32 (device): sequence s is the rows
+        offsets[s]..offsets[s+1], the chosen sequences first, then the
+        rejected ones; ref_logprobs [2 pairs] a reference model's sums."""
+        torch = _torch()
+        s = self._input(logits, tokens, temperature)
+        if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 \
+                or offsets.numel() % 2 != 1:
+            raise ValueError("offsets must be a 1-D tensor of 2 * pairs + 1 values")
+        pairs = offsets.numel() // 2
+        p = Preference(self._vector(offsets, 2 * pairs + 1, torch.int32, "offsets"), pairs,
+                       self._vector(ref_logprobs, 2 * pairs, torch.float32, "ref_logprobs"),
+                       beta, label_smoothing, margin, int(average), scale)
+        d, ptr, ldd = self._gradient(logits, out) if grad else (None, None, 0)
+        loss, losses, seq, lp = (self._new(1), self._new(pairs), self._new(2 * pairs),
+                                 self._new(s.rows))
+        _check(_lib().eb_preference_loss(self._h, C.byref(s), C.byref(p), loss.data_ptr(),
+                                         losses.data_ptr(), seq.data_ptr(), lp.data_ptr(), ptr,
+                                         ldd, self._stream()), "eb_preference_loss")
+        return PreferenceLoss(loss, losses, seq, lp, d)
+
+    def lmhead_logprobs(self, hidden, weight, tokens, temperature=1.0, entropies: bool = True):
+        """token_logprobs on the logits hidden @ weight^T (bf16 [rows, d] or
+        [B, L, d], and [V, d]) without forming them in memory."""
+        torch = _torch()
+        for t, n in ((hidden, "hidden"), (weight, "weight")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{n} must be a torch tensor")
+            if t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != self.device:
+                raise ValueError(f"{n} must be a contiguous bf16 tensor on {self.device}")
+        if hidden.dim() < 2 or weight.dim() != 2 or weight.shape[1] != hidden.shape[-1]:
+            raise ValueError("hidden must be [rows, d] and weight [V, d]")
+        V, d = weight.shape
+        rows = hidden.numel() // d if d else 0
+        lp = self._new(rows)
+        h = self._new(rows) if entropies else None
+        tensor = isinstance(temperature, torch.Tensor)
+        _check(_lib().eb_lmhead_logprobs(
+            self._h, hidden.data_ptr(), weight.data_ptr(), rows, V, d,
+            self._vector(tokens, rows, torch.int32, "tokens"),
+            self._vector(temperature, rows, torch.float32, "temperature") if tensor else None,
+            1.0 if tensor else float(temperature), lp.data_ptr(),
+            h.data_ptr() if entropies else None, self._stream()), "eb_lmhead_logprobs")
+        return TokenScores(lp, h)
+
+    def status(self, clear: bool = False) -> int:
+        s = C.c_uint32(0)
+        _check(_lib().eb_scorer_status(self._h, C.byref(s), int(clear), self._stream()),
+               "eb_scorer_status")
+        return int(s.value)
+
+    def set_wait_limit(self, limit_ns: int = 0):
+        """Limit (ns) of the internal waits; 0 = the default 2 s (a diagnostic
+        hook, see include/eb_sampler.h)."""
+        _check(_lib().eb_scorer_set_wait_limit(self._h, int(limit_ns)),
+               "eb_scorer_set_wait_limit")
+
+    def workspace_bytes(self) -> int:
+        return int(_lib().eb_scorer_workspace_bytes(self._h))
+
+    def close(self):
+        if getattr(self, "_h", None):
+            _lib().eb_scorer_destroy(self._h)
             self._h = None
 
     def __del__(self):

@@ -1,0 +1,391 @@
+// eb_score.cu -- host side of the scorer (eb_scorer_*, eb_token_logprobs*,
+// eb_policy_loss, eb_preference_loss, eb_lmhead_logprobs of
+// include/eb_sampler.h): validation, workspace, launches.
+#include "eb_sampler.h"
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <functional>
+#include <mutex>
+#include <new>
+
+#include "eb_host.cuh"
+#include "eb_lmscore.cuh"
+#include "eb_score.cuh"
+
+using ebk::DeviceGuard;
+using ebk::ScoreArgs;
+using ebk::align256;
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+constexpr int kMaxGrid = 2048;  // CTAs of a policy launch (partial sums kept for each)
+
+struct DeviceInfo {
+  std::once_flag once;
+  int rc = EB_ERR_CUDA;
+  int sms = 0;
+  size_t optin = 0;
+};
+DeviceInfo g_info[kMaxDevices];
+
+void info_setup(DeviceInfo& d, int device) {
+  int sms = 0, optin = 0, major = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device) !=
+          cudaSuccess ||
+      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device) != cudaSuccess) {
+    cudaGetLastError();
+    d.rc = EB_ERR_CUDA;
+    return;
+  }
+  if (major != 10) {
+    d.rc = EB_ERR_UNSUPPORTED;
+    return;
+  }
+  if (cudaFuncSetAttribute(ebk::lmscore_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           optin) != cudaSuccess) {
+    cudaGetLastError();
+    d.rc = EB_ERR_CUDA;
+    return;
+  }
+  d.sms = sms;
+  d.optin = (size_t)optin;
+  d.rc = EB_OK;
+}
+
+}  // namespace
+
+struct eb_scorer {
+  int device = 0;
+  int max_rows = 0;
+  int sms = 0;
+  size_t optin = 0;
+  uint64_t wait_ns = ebk::kWaitLimitNs;
+  void* ws = nullptr;
+  size_t ws_bytes = 0;
+  uint32_t* status = nullptr;
+  uint32_t* counter = nullptr;
+  double* part = nullptr;           // [kMaxGrid][terms]
+  float* lp = nullptr;              // [max_rows] log-probabilities (preference)
+  float* g = nullptr;               // [max_rows] their gradients (preference)
+  ebk::LmSums* lm = nullptr;        // [lm_slots] the LM-head pass's partial sums
+  float* lm_za = nullptr;           // [max_rows] the tokens' logits
+  size_t lm_slots = 0;
+};
+
+namespace {
+
+size_t elt_bytes(int dtype) { return dtype == EB_F32 ? 4 : 2; }
+
+// Sizes, types and pointers every call over logits shares.
+int check_input(const eb_scorer* h, const eb_score_input_t* in) {
+  if (!h || !in) return EB_ERR_INVALID_ARG;
+  if (in->dtype != EB_F32 && in->dtype != EB_BF16) return EB_ERR_UNSUPPORTED;
+  if (in->rows < 0 || in->V < 1 || in->ld < in->V) return EB_ERR_INVALID_ARG;
+  if (in->rows > h->max_rows || in->V > (1 << 30) || in->ld > (1ll << 40)) return EB_ERR_OVERFLOW;
+  if (in->rows > 0 && (!in->logits || !in->tokens)) return EB_ERR_INVALID_ARG;
+  if ((uintptr_t)in->logits % elt_bytes(in->dtype) != 0) return EB_ERR_INVALID_ARG;
+  if (!in->temperatures && !(in->temperature > 0.0 && std::isfinite(in->temperature)))
+    return EB_ERR_INVALID_ARG;
+  return EB_OK;
+}
+
+// A gradient may be written over its own logits (same address and stride).
+int check_grad(const eb_score_input_t* in, const void* d_logits, int64_t ldd) {
+  if (ldd < in->V) return EB_ERR_INVALID_ARG;
+  if (ldd > (1ll << 40)) return EB_ERR_OVERFLOW;
+  if ((uintptr_t)d_logits % elt_bytes(in->dtype) != 0) return EB_ERR_INVALID_ARG;
+  if (in->rows > 1 && d_logits == in->logits && ldd != in->ld) return EB_ERR_INVALID_ARG;
+  return EB_OK;
+}
+
+void fill_args(const eb_scorer* h, const eb_score_input_t* in, ScoreArgs& a) {
+  std::memset(&a, 0, sizeof(a));
+  a.logits = in->logits;
+  a.ld = in->ld;
+  a.rows = in->rows;
+  a.V = in->V;
+  a.tokens = in->tokens;
+  a.temps = in->temperatures;
+  a.temp = (float)in->temperature;
+  a.part = h->part;
+  a.counter = h->counter;
+  a.status = h->status;
+}
+
+int launch_rows(const eb_scorer* h, const ScoreArgs& a, int dtype, int mode, bool reverse,
+                cudaStream_t st) {
+  const int grid = std::max(1, std::min(a.rows, 4 * h->sms));
+  if (dtype == EB_F32)
+    ebk::score_rows_kernel<ebk::kScoreF32><<<grid, ebk::kRowThreads, 0, st>>>(a, mode, reverse);
+  else
+    ebk::score_rows_kernel<ebk::kScoreBF16><<<grid, ebk::kRowThreads, 0, st>>>(a, mode, reverse);
+  return cudaGetLastError() == cudaSuccess ? EB_OK : EB_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int eb_scorer_init(eb_scorer_t** out, int32_t max_rows, int device) {
+  if (!out) return EB_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (max_rows < 1) return EB_ERR_INVALID_ARG;
+  if (max_rows > EB_MAX_SCORE_ROWS) return EB_ERR_OVERFLOW;
+  int ndev = 0;
+  if (cudaGetDeviceCount(&ndev) != cudaSuccess) return EB_ERR_CUDA;
+  if (device < 0 || device >= ndev) return EB_ERR_INVALID_ARG;
+  if (device >= kMaxDevices) return EB_ERR_UNSUPPORTED;
+  DeviceGuard guard(device);
+  if (!guard.ok) return EB_ERR_CUDA;
+  DeviceInfo& d = g_info[device];
+  std::call_once(d.once, info_setup, std::ref(d), device);
+  if (d.rc != EB_OK) return d.rc;
+
+  eb_scorer* h = new (std::nothrow) eb_scorer();
+  if (!h) return EB_ERR_OUT_OF_MEMORY;
+  h->device = device;
+  h->max_rows = max_rows;
+  h->sms = d.sms;
+  h->optin = d.optin;
+  h->lm_slots = ebk::lm_score_slots(d.sms, max_rows);
+  size_t off = 0;
+  const size_t o_status = off;
+  off = align256(off + 2 * sizeof(uint32_t));
+  const size_t o_part = off;
+  off = align256(off + sizeof(double) * kMaxGrid * ebk::kPolicyTerms);
+  const size_t o_lp = off;
+  off = align256(off + sizeof(float) * (size_t)max_rows);
+  const size_t o_g = off;
+  off = align256(off + sizeof(float) * (size_t)max_rows);
+  const size_t o_lm = off;
+  off = align256(off + sizeof(ebk::LmSums) * h->lm_slots);
+  const size_t o_za = off;
+  off = align256(off + sizeof(float) * (size_t)max_rows);
+  h->ws_bytes = off;
+  if (cudaMalloc(&h->ws, h->ws_bytes) != cudaSuccess) {
+    cudaGetLastError();
+    delete h;
+    return EB_ERR_OUT_OF_MEMORY;
+  }
+  if (cudaMemset(h->ws, 0, h->ws_bytes) != cudaSuccess) {
+    cudaFree(h->ws);
+    delete h;
+    return EB_ERR_CUDA;
+  }
+  char* base = static_cast<char*>(h->ws);
+  h->status = reinterpret_cast<uint32_t*>(base + o_status);
+  h->counter = h->status + 1;
+  h->part = reinterpret_cast<double*>(base + o_part);
+  h->lp = reinterpret_cast<float*>(base + o_lp);
+  h->g = reinterpret_cast<float*>(base + o_g);
+  h->lm = reinterpret_cast<ebk::LmSums*>(base + o_lm);
+  h->lm_za = reinterpret_cast<float*>(base + o_za);
+  *out = h;
+  return EB_OK;
+}
+
+int eb_token_logprobs(eb_scorer_t* h, const eb_score_input_t* in, float* logprobs,
+                      float* entropies, void* stream) {
+  int rc = check_input(h, in);
+  if (rc != EB_OK) return rc;
+  if (in->rows == 0) return EB_OK;
+  if (!logprobs) return EB_ERR_INVALID_ARG;
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return EB_ERR_CUDA;
+  ScoreArgs a;
+  fill_args(h, in, a);
+  a.logprobs = logprobs;
+  a.entropies = entropies;
+  return launch_rows(h, a, in->dtype, ebk::kModeScore, false, (cudaStream_t)stream);
+}
+
+int eb_token_logprobs_backward(eb_scorer_t* h, const eb_score_input_t* in,
+                               const float* d_logprobs, const float* d_entropies, void* d_logits,
+                               int64_t ldd, void* stream) {
+  int rc = check_input(h, in);
+  if (rc != EB_OK) return rc;
+  if ((rc = check_grad(in, d_logits, ldd)) != EB_OK) return rc;
+  if (in->rows == 0) return EB_OK;
+  if (!d_logprobs || !d_logits) return EB_ERR_INVALID_ARG;
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return EB_ERR_CUDA;
+  ScoreArgs a;
+  fill_args(h, in, a);
+  a.d_logits = d_logits;
+  a.ldd = ldd;
+  a.g_lp = d_logprobs;
+  a.g_h = d_entropies;
+  return launch_rows(h, a, in->dtype, ebk::kModeGrad, false, (cudaStream_t)stream);
+}
+
+int eb_policy_loss(eb_scorer_t* h, const eb_score_input_t* in, const eb_policy_t* p, float* terms,
+                   float* logprobs, float* entropies, void* d_logits, int64_t ldd, void* stream) {
+  int rc = check_input(h, in);
+  if (rc != EB_OK) return rc;
+  if (!p || !terms) return EB_ERR_INVALID_ARG;
+  if (!(p->clip_low >= 0.0 && p->clip_low <= 1.0) || !(p->clip_high >= 0.0) ||
+      !std::isfinite(p->clip_high) || !std::isfinite(p->kl_coef) ||
+      !std::isfinite(p->entropy_coef) || !std::isfinite(p->scale))
+    return EB_ERR_INVALID_ARG;
+  if (p->kl_coef != 0.0 && !p->ref_logprobs && in->rows > 0) return EB_ERR_INVALID_ARG;
+  if (in->rows > 0 && (!p->old_logprobs || !p->advantages)) return EB_ERR_INVALID_ARG;
+  if (d_logits && (rc = check_grad(in, d_logits, ldd)) != EB_OK) return rc;
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return EB_ERR_CUDA;
+  ScoreArgs a;
+  fill_args(h, in, a);
+  a.logprobs = logprobs;
+  a.entropies = entropies;
+  a.d_logits = d_logits;
+  a.ldd = ldd;
+  a.old_lp = p->old_logprobs;
+  a.ref_lp = p->ref_logprobs;
+  a.adv = p->advantages;
+  a.weights = p->weights;
+  a.clip_lo = (float)(1.0 - p->clip_low);
+  a.clip_hi = (float)(1.0 + p->clip_high);
+  a.kl_coef = (float)p->kl_coef;
+  a.ent_coef = (float)p->entropy_coef;
+  a.scale = p->scale;
+  a.terms = terms;
+  return launch_rows(h, a, in->dtype, ebk::kModePolicy, false, (cudaStream_t)stream);
+}
+
+int eb_preference_loss(eb_scorer_t* h, const eb_score_input_t* in, const eb_preference_t* p,
+                       float* loss, float* losses, float* sequence_logprobs, float* logprobs,
+                       void* d_logits, int64_t ldd, void* stream) {
+  int rc = check_input(h, in);
+  if (rc != EB_OK) return rc;
+  if (!p || !loss || p->pairs < 0) return EB_ERR_INVALID_ARG;
+  if (p->pairs > EB_MAX_SCORE_ROWS) return EB_ERR_OVERFLOW;
+  if (!(p->beta >= 0.0) || !std::isfinite(p->beta) ||
+      !(p->label_smoothing >= 0.0 && p->label_smoothing < 1.0) || !std::isfinite(p->margin) ||
+      !std::isfinite(p->scale) || (p->average != 0 && p->average != 1))
+    return EB_ERR_INVALID_ARG;
+  if (!p->offsets || (p->pairs > 0 && (!losses || !sequence_logprobs))) return EB_ERR_INVALID_ARG;
+  if (d_logits && (rc = check_grad(in, d_logits, ldd)) != EB_OK) return rc;
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return EB_ERR_CUDA;
+  cudaStream_t st = (cudaStream_t)stream;
+  ScoreArgs a;
+  fill_args(h, in, a);
+  a.offsets = p->offsets;
+  a.n_off = 2 * p->pairs;
+  a.logprobs = logprobs ? logprobs : h->lp;
+  if (in->rows > 0 &&
+      (rc = launch_rows(h, a, in->dtype, ebk::kModeScore, false, st)) != EB_OK)
+    return rc;
+  if (p->pairs == 0) {
+    if (cudaMemsetAsync(loss, 0, sizeof(float), st) != cudaSuccess) return EB_ERR_CUDA;
+  } else {
+    ebk::PrefArgs q;
+    q.lp = a.logprobs;
+    q.tokens = in->tokens;
+    q.offsets = p->offsets;
+    q.ref = p->ref_logprobs;
+    q.rows = in->rows;
+    q.pairs = p->pairs;
+    q.average = p->average;
+    q.beta = p->beta;
+    q.smooth = p->label_smoothing;
+    q.margin = p->margin;
+    q.scale = p->scale;
+    q.loss = loss;
+    q.losses = losses;
+    q.seq = sequence_logprobs;
+    q.g_lp = d_logits ? h->g : nullptr;
+    q.counter = h->counter;
+    q.status = h->status;
+    ebk::preference_kernel<<<p->pairs, ebk::kPrefThreads, 0, st>>>(q);
+    if (cudaGetLastError() != cudaSuccess) return EB_ERR_CUDA;
+  }
+  if (!d_logits || in->rows == 0) return EB_OK;
+  a.logprobs = nullptr;
+  a.d_logits = d_logits;
+  a.ldd = ldd;
+  a.g_lp = h->g;
+  return launch_rows(h, a, in->dtype, ebk::kModeGrad, true, st);
+}
+
+int eb_lmhead_logprobs(eb_scorer_t* h, const void* hidden, const void* weight, int32_t rows,
+                       int32_t V, int32_t d, const int32_t* tokens, const float* temperatures,
+                       double temperature, float* logprobs, float* entropies, void* stream) {
+  if (!h || rows < 0 || V < 1 || d < 1) return EB_ERR_INVALID_ARG;
+  if (d % 8 != 0) return EB_ERR_UNSUPPORTED;
+  if (rows > h->max_rows || V > (1 << 30) || d > (1 << 20)) return EB_ERR_OVERFLOW;
+  if (!temperatures && !(temperature > 0.0 && std::isfinite(temperature)))
+    return EB_ERR_INVALID_ARG;
+  if (rows == 0) return EB_OK;
+  if (!hidden || !weight || !tokens || !logprobs) return EB_ERR_INVALID_ARG;
+  if ((uintptr_t)hidden % 16 != 0 || (uintptr_t)weight % 16 != 0) return EB_ERR_INVALID_ARG;
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return EB_ERR_CUDA;
+  cudaStream_t st = (cudaStream_t)stream;
+  ebk::LmScoreArgs p;
+  std::memset(&p, 0, sizeof(p));
+  p.tokens = tokens;
+  p.temps = temperatures;
+  p.temp = (float)temperature;
+  p.sums = h->lm;
+  p.za = h->lm_za;
+  p.rows = rows;
+  p.V = V;
+  p.d = d;
+  p.n_split = ebk::lm_score_split(h->sms, rows, V);
+  p.wait_ns = h->wait_ns;
+  p.status = h->status;
+  p.logprobs = logprobs;
+  p.entropies = entropies;
+  if ((size_t)p.n_split * (size_t)rows > h->lm_slots) return EB_ERR_OVERFLOW;
+  CUtensorMap th, tw;
+  if (!ebk::make_tmap(&th, hidden, (uint64_t)d, (uint64_t)rows, ebk::kLsBK, ebk::kLsBM) ||
+      !ebk::make_tmap(&tw, weight, (uint64_t)d, (uint64_t)V, ebk::kLsBK, ebk::kLsBN))
+    return EB_ERR_CUDA;
+  const size_t smem = ebk::lm_score_layout().total;
+  if (smem > h->optin) return EB_ERR_UNSUPPORTED;
+  const int n_mt = (rows + ebk::kLsBM - 1) / ebk::kLsBM;
+  ebk::lmscore_kernel<<<n_mt * p.n_split, ebk::kLsThreads, smem, st>>>(th, tw, p);
+  if (cudaGetLastError() != cudaSuccess) return EB_ERR_CUDA;
+  ebk::lmscore_finish_kernel<<<(rows + 127) / 128, 128, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? EB_OK : EB_ERR_CUDA;
+}
+
+int eb_scorer_status(eb_scorer_t* h, uint32_t* status, int clear, void* stream) {
+  if (!h || !status) return EB_ERR_INVALID_ARG;
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return EB_ERR_CUDA;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (cudaMemcpyAsync(status, h->status, sizeof(uint32_t), cudaMemcpyDeviceToHost, st) !=
+      cudaSuccess)
+    return EB_ERR_CUDA;
+  if (clear && cudaMemsetAsync(h->status, 0, sizeof(uint32_t), st) != cudaSuccess)
+    return EB_ERR_CUDA;
+  if (cudaStreamSynchronize(st) != cudaSuccess) return EB_ERR_CUDA;
+  return EB_OK;
+}
+
+int eb_scorer_set_wait_limit(eb_scorer_t* h, uint64_t limit_ns) {
+  if (!h) return EB_ERR_INVALID_ARG;
+  h->wait_ns = limit_ns == 0 ? ebk::kWaitLimitNs : limit_ns;
+  return EB_OK;
+}
+
+size_t eb_scorer_workspace_bytes(const eb_scorer_t* h) { return h ? h->ws_bytes : 0; }
+
+void eb_scorer_destroy(eb_scorer_t* h) {
+  if (!h) return;
+  {
+    DeviceGuard guard(h->device);
+    if (h->ws) cudaFree(h->ws);
+  }
+  delete h;
+}
+
+}  // extern "C"

@@ -83,9 +83,11 @@ enum {
 
 /* Bits of the device status word. */
 enum {
-  EB_STATUS_BAD_TOKEN = 1,   /* a committed position held a token outside [0, V) */
+  EB_STATUS_BAD_TOKEN = 1,   /* a committed position held a token outside [0, V); a scorer's
+                                row had a token >= V */
   EB_STATUS_NONFINITE = 2,   /* a row produced a non-finite softmax sum */
-  EB_STATUS_TIMEOUT = 4      /* an internal bounded wait gave up */
+  EB_STATUS_TIMEOUT = 4,     /* an internal bounded wait gave up */
+  EB_STATUS_BAD_OFFSETS = 8  /* eb_preference_loss: offsets not in order or outside the rows */
 };
 
 /* Stop reasons written to stop_flags. */
@@ -333,6 +335,155 @@ size_t eb_sampler_workspace_bytes(const eb_sampler_t* h);
 
 /* Release the workspace and the handle (NULL is allowed). */
 void eb_sampler_destroy(eb_sampler_t* h);
+
+/* ---------------------------------------------------------------------------
+ * Scoring the tokens a sampler committed, and the losses that learn from
+ * them.  A row is one position: its logits z [V], its token a and its
+ * temperature T.  With p = softmax(z / T), every call is about
+ *     log p_a  (nats)   and   H = -sum_v p_v ln p_v  (nats),
+ * the quantities eb_sampler_step draws from and decides on, now for a token
+ * given by the caller.  No counterpart in the DiffusionGemma pages, which
+ * describe decoding only.
+ *
+ * Conventions, besides those at the top of this file:
+ *   - A scorer handle owns a workspace for up to max_rows rows; one handle per
+ *     stream at a time (two graphs captured with one handle must not run at
+ *     the same time).  Calls allocate nothing, never synchronise and can be
+ *     captured in a CUDA graph.
+ *   - logits [rows][ld] fp32 or bf16, row i at element i ld, ld >= V; any
+ *     alignment to the element (rows aligned to 16 bytes load faster).
+ *     Logits may be -inf (probability 0); NaN, +inf or a row of only -inf
+ *     gives NaN results and sets EB_STATUS_NONFINITE.
+ *   - tokens [rows] int32.  A negative token, a policy weight of 0 or (in
+ *     eb_preference_loss) a place outside the sequences makes a row ignored:
+ *     its logits are not read, its log-probability and entropy are written
+ *     as 0 and its gradient as zeros.  A token >= V gives NaN results and
+ *     sets EB_STATUS_BAD_TOKEN.
+ *   - temperatures [rows] fp32 (device), or NULL: `temperature` for every
+ *     row (finite, > 0).  A per-row temperature that is not finite and
+ *     positive gives NaN results and sets EB_STATUS_NONFINITE.
+ *   - Log-probabilities near 0 (p_a near 1) keep their relative precision.
+ *   - d_logits [rows][ldd], the logits' type, each element rounded once;
+ *     elements past V of a row are left as they are.  It may be the logits
+ *     themselves (same address, ldd = ld: the gradient replaces them), and
+ *     must not overlap them otherwise.
+ *   - Results are the same bits at every call with the same inputs on one
+ *     device.
+ */
+typedef struct eb_scorer eb_scorer_t;
+
+#define EB_MAX_SCORE_ROWS (1 << 24)
+#define EB_POLICY_TERMS 5
+
+typedef struct {
+  const void* logits;        /* [rows][ld], see above */
+  int32_t dtype;             /* eb_dtype_t */
+  int32_t rows;              /* >= 0, at most the handle's max_rows */
+  int32_t V;                 /* vocabulary size, 1 .. 2^30 */
+  int64_t ld;                /* elements between rows, >= V */
+  const int32_t* tokens;     /* [rows] */
+  const float* temperatures; /* [rows] or NULL */
+  double temperature;        /* used when temperatures is NULL */
+} eb_score_input_t;
+
+/* Create a scorer on CUDA device `device` (sm_100) for calls of up to
+   max_rows rows (1 .. EB_MAX_SCORE_ROWS); one device allocation.
+   Errors: INVALID_ARG, OVERFLOW, UNSUPPORTED, OUT_OF_MEMORY, CUDA. */
+int eb_scorer_init(eb_scorer_t** out, int32_t max_rows, int device);
+
+/* logprobs [rows] = log p_a and, unless NULL, entropies [rows] = H, fp32. */
+int eb_token_logprobs(eb_scorer_t* h, const eb_score_input_t* in, float* logprobs,
+                      float* entropies, void* stream);
+
+/* The gradient of sum_i (d_logprobs[i] log p_a + d_entropies[i] H) for the
+   logits: d_logits = (1/T) [ g (onehot_a - p) - h p (ln p + H) ].
+   d_logprobs [rows] fp32; d_entropies [rows] fp32 or NULL (zeros).  Needs
+   nothing from the forward call: the rows' sums are formed again from the
+   same read of the logits. */
+int eb_token_logprobs_backward(eb_scorer_t* h, const eb_score_input_t* in,
+                               const float* d_logprobs, const float* d_entropies, void* d_logits,
+                               int64_t ldd, void* stream);
+
+/* Clipped policy loss with a KL term and an entropy bonus.  Per row, with
+   r = exp(log p_a - old), A the advantage and w the weight:
+     pg = max(-A r, -A min(max(r, 1 - clip_low), 1 + clip_high))
+     KL = exp(ref - log p_a) - 1 - (ref - log p_a)   (0 without ref_logprobs)
+     loss = scale sum_i w (pg + kl_coef KL - entropy_coef H)
+   A normalisation (a mean over tokens or sequences) goes into scale and the
+   weights. */
+typedef struct {
+  const float* old_logprobs; /* [rows] log p_a when the tokens were drawn */
+  const float* advantages;   /* [rows] */
+  const float* ref_logprobs; /* [rows] log p_a of a reference model, or NULL (then kl_coef = 0) */
+  const float* weights;      /* [rows] w, or NULL: 1 */
+  double clip_low;           /* 0 .. 1 */
+  double clip_high;          /* >= 0 */
+  double kl_coef, entropy_coef, scale;
+} eb_policy_t;
+
+/* terms [EB_POLICY_TERMS] fp32: the loss, then scale sum w of pg, KL, H, and
+   of 1 where the clipped side is the larger (its gradient is cut).
+   logprobs, entropies [rows] fp32: as eb_token_logprobs, either may be NULL.
+   d_logits: the loss's gradient for the logits, or NULL: no gradient. */
+int eb_policy_loss(eb_scorer_t* h, const eb_score_input_t* in, const eb_policy_t* policy,
+                   float* terms, float* logprobs, float* entropies, void* d_logits, int64_t ldd,
+                   void* stream);
+
+/* Preference loss over pairs of sequences.  Sequence s is the rows
+   offsets[s] .. offsets[s+1]; 0 .. pairs-1 are the chosen ones, pairs ..
+   2 pairs - 1 the rejected ones, pair k being (k, pairs + k).  With S the
+   sum of a sequence's log p_a over its rows with token >= 0 (average = 1:
+   the mean) and ref the same of a reference model:
+     m_k  = beta ((S_k - ref_k) - (S_{P+k} - ref_{P+k})) - margin
+     loss = scale sum_k [ -(1 - label_smoothing) ln sigmoid(m_k)
+                          - label_smoothing ln sigmoid(-m_k) ]
+   An empty sequence has S = 0. */
+typedef struct {
+  const int32_t* offsets;    /* [2 pairs + 1] device, ascending, within 0 .. rows */
+  int32_t pairs;             /* >= 0 */
+  const float* ref_logprobs; /* [2 pairs] device, or NULL: zeros */
+  double beta;               /* >= 0 */
+  double label_smoothing;    /* 0 <= . < 1 */
+  double margin;
+  int32_t average;           /* 0 or 1 */
+  double scale;
+} eb_preference_t;
+
+/* loss [1], losses [pairs], sequence_logprobs [2 pairs] (S) fp32;
+   logprobs [rows] fp32 or NULL; d_logits: the loss's gradient for the
+   logits, or NULL: no gradient.  Offsets out of order or range set
+   EB_STATUS_BAD_OFFSETS and make their pair's loss NaN; nothing outside the
+   buffers is touched. */
+int eb_preference_loss(eb_scorer_t* h, const eb_score_input_t* in,
+                       const eb_preference_t* preference, float* loss, float* losses,
+                       float* sequence_logprobs, float* logprobs, void* d_logits, int64_t ldd,
+                       void* stream);
+
+/* eb_token_logprobs on z = hidden weight^T without forming the logits in
+   memory (tensor cores, bf16 in, fp32 accumulate, as in eb_lmhead_step):
+   scoring under a policy or a reference model.
+     hidden [rows][d] bf16, weight [V][d] bf16, device memory, 16-byte
+     aligned, row-major, read only; d a multiple of 8 (EB_ERR_UNSUPPORTED
+     otherwise), any V >= 1, rows up to max_rows; an ignored row still takes
+     part in the product. */
+int eb_lmhead_logprobs(eb_scorer_t* h, const void* hidden, const void* weight, int32_t rows,
+                       int32_t V, int32_t d, const int32_t* tokens, const float* temperatures,
+                       double temperature, float* logprobs, float* entropies, void* stream);
+
+/* Synchronise `stream` and read the scorer's status word (EB_STATUS_* bits,
+   kept until cleared); clear it when `clear` is non-zero. */
+int eb_scorer_status(eb_scorer_t* h, uint32_t* status, int clear, void* stream);
+
+/* Diagnostic hook: the limit, in nanoseconds, of the scorer's internal waits
+   (0 = the default of 2 s).  A wait that runs out sets EB_STATUS_TIMEOUT; the
+   call's results are then NaN or unwritten, and the device stays usable. */
+int eb_scorer_set_wait_limit(eb_scorer_t* h, uint64_t limit_ns);
+
+/* Bytes of device workspace the scorer holds. */
+size_t eb_scorer_workspace_bytes(const eb_scorer_t* h);
+
+/* Release the workspace and the handle (NULL is allowed). */
+void eb_scorer_destroy(eb_scorer_t* h);
 
 /* Static description of a status code. */
 const char* eb_strerror(int code);
