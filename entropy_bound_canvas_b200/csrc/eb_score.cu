@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -26,11 +27,41 @@ namespace {
 constexpr int kMaxDevices = 64;
 constexpr int kMaxGrid = 2048;  // CTAs of a policy launch (partial sums kept for each)
 
+// The row kernel's variants: [bf16][entropy][gradient][wide].
+template <int DT, bool ENT, bool GRAD, int NW>
+const void* ring_fn() {
+  return reinterpret_cast<const void*>(&ebk::score_ring_kernel<DT, ENT, GRAD, NW>);
+}
+constexpr int kRingVariants = 16;
+const void* const kRing[kRingVariants] = {
+    ring_fn<ebk::kScoreF32, false, false, 4>(),  ring_fn<ebk::kScoreF32, false, false, 8>(),
+    ring_fn<ebk::kScoreF32, false, true, 4>(),   ring_fn<ebk::kScoreF32, false, true, 8>(),
+    ring_fn<ebk::kScoreF32, true, false, 4>(),   ring_fn<ebk::kScoreF32, true, false, 8>(),
+    ring_fn<ebk::kScoreF32, true, true, 4>(),    ring_fn<ebk::kScoreF32, true, true, 8>(),
+    ring_fn<ebk::kScoreBF16, false, false, 4>(), ring_fn<ebk::kScoreBF16, false, false, 8>(),
+    ring_fn<ebk::kScoreBF16, false, true, 4>(),  ring_fn<ebk::kScoreBF16, false, true, 8>(),
+    ring_fn<ebk::kScoreBF16, true, false, 4>(),  ring_fn<ebk::kScoreBF16, true, false, 8>(),
+    ring_fn<ebk::kScoreBF16, true, true, 4>(),   ring_fn<ebk::kScoreBF16, true, true, 8>()};
+int ring_variant(bool bf16, bool ent, bool grad, bool wide) {
+  return (bf16 ? 8 : 0) + (ent ? 4 : 0) + (grad ? 2 : 0) + (wide ? 1 : 0);
+}
+
+// Two wide CTAs (13 stages, 104 KB) or six narrow ones (4 stages, 32 KB)
+// share an SM.
+constexpr int kWideStages = 13, kNarrowStages = 4;
+size_t ring_smem_of(bool wide) {
+  return wide ? ebk::ring_smem(kWideStages, 8) : ebk::ring_smem(kNarrowStages, 4);
+}
+constexpr int64_t kNarrowBytes = 16384;  // rows up to this take the narrow form
+constexpr int kShareStages = 8;          // a wide CTA's share where the cluster allows it
+constexpr int kMaxC = 8;
+
 struct DeviceInfo {
   std::once_flag once;
   int rc = EB_ERR_CUDA;
   int sms = 0;
   size_t optin = 0;
+  std::atomic<int> clusters[kRingVariants][5];
 };
 DeviceInfo g_info[kMaxDevices];
 
@@ -53,6 +84,19 @@ void info_setup(DeviceInfo& d, int device) {
     cudaGetLastError();
     d.rc = EB_ERR_CUDA;
     return;
+  }
+  for (int v = 0; v < kRingVariants; ++v) {
+    const size_t smem = ring_smem_of(v & 1);
+    if (smem > (size_t)optin) {
+      d.rc = EB_ERR_UNSUPPORTED;
+      return;
+    }
+    if (cudaFuncSetAttribute(kRing[v], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      d.rc = EB_ERR_CUDA;
+      return;
+    }
   }
   d.sms = sms;
   d.optin = (size_t)optin;
@@ -117,16 +161,73 @@ void fill_args(const eb_scorer* h, const eb_score_input_t* in, ScoreArgs& a) {
   a.part = h->part;
   a.counter = h->counter;
   a.status = h->status;
+  a.wait_ns = h->wait_ns;
 }
 
-int launch_rows(const eb_scorer* h, const ScoreArgs& a, int dtype, int mode, bool reverse,
-                cudaStream_t st) {
-  const int grid = std::max(1, std::min(a.rows, 4 * h->sms));
-  if (dtype == EB_F32)
-    ebk::score_rows_kernel<ebk::kScoreF32><<<grid, ebk::kRowThreads, 0, st>>>(a, mode, reverse);
-  else
-    ebk::score_rows_kernel<ebk::kScoreBF16><<<grid, ebk::kRowThreads, 0, st>>>(a, mode, reverse);
-  return cudaGetLastError() == cudaSuccess ? EB_OK : EB_ERR_CUDA;
+// How a launch over rows is laid out.
+struct RingPlan {
+  int wide;      // 8 consumer warps and a large ring, else 4 and a small one
+  int C;         // CTAs per row
+  int resident;  // a CTA's share of a row fits its ring
+};
+
+int share_stages(int64_t row_bytes, int C) {
+  // the aligned image of a row spans up to one granule more than its bytes
+  const int64_t G = (row_bytes + 15) / 16 + 1;
+  const int64_t per = ((G + C - 1) / C + 7) / 8 * 8;
+  return (int)std::min<int64_t>((per + ebk::kStageGran - 1) / ebk::kStageGran, 1 << 20);
+}
+
+RingPlan ring_plan(int sms, int64_t rows, int64_t row_bytes) {
+  RingPlan r;
+  r.wide = row_bytes > kNarrowBytes;
+  r.C = 1;
+  if (r.wide) {
+    while (r.C < kMaxC && share_stages(row_bytes, r.C) > kShareStages) r.C *= 2;
+    while (r.C < kMaxC && rows * r.C * 2 <= 2 * sms && row_bytes / r.C > 2 * ebk::kStageBytes)
+      r.C *= 2;
+  }
+  r.resident = share_stages(row_bytes, r.C) <= (r.wide ? kWideStages : kNarrowStages);
+  return r;
+}
+
+int launch_rows(const eb_scorer* h, const ScoreArgs& a, int dtype, int mode, bool ent, bool grad,
+                bool reverse, cudaStream_t st) {
+  const RingPlan r = ring_plan(h->sms, a.rows, (int64_t)a.V * (int64_t)elt_bytes(dtype));
+  const int v = ring_variant(dtype == EB_BF16, ent, grad, r.wide);
+  const int warps = r.wide ? 8 : 4;
+  ebk::RingArgs q;
+  q.mode = mode;
+  q.reverse = reverse ? 1 : 0;
+  q.C = r.C;
+  q.stages = r.wide ? kWideStages : kNarrowStages;
+  q.resident = r.resident;
+  cudaLaunchConfig_t lc;
+  std::memset(&lc, 0, sizeof(lc));
+  lc.blockDim = dim3((warps + 1) * 32);
+  lc.dynamicSmemBytes = ring_smem_of(r.wide);
+  lc.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = r.C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  // the clusters that fit the device at once, asked once per variant and size
+  std::atomic<int>& cached = g_info[h->device].clusters[v][__builtin_ctz(r.C)];
+  int most = cached.load(std::memory_order_relaxed);
+  if (most == 0) {
+    lc.gridDim = dim3(r.C);
+    if (cudaOccupancyMaxActiveClusters(&most, kRing[v], &lc) != cudaSuccess || most < 1) {
+      cudaGetLastError();
+      return EB_ERR_CUDA;
+    }
+    most = std::min(most, kMaxGrid);
+    cached.store(most, std::memory_order_relaxed);
+  }
+  lc.gridDim = dim3(std::max(1, std::min(a.rows, most)) * r.C);
+  void* args[] = {const_cast<ScoreArgs*>(&a), &q};
+  return cudaLaunchKernelExC(&lc, kRing[v], args) == cudaSuccess ? EB_OK : EB_ERR_CUDA;
 }
 
 }  // namespace
@@ -203,7 +304,8 @@ int eb_token_logprobs(eb_scorer_t* h, const eb_score_input_t* in, float* logprob
   fill_args(h, in, a);
   a.logprobs = logprobs;
   a.entropies = entropies;
-  return launch_rows(h, a, in->dtype, ebk::kModeScore, false, (cudaStream_t)stream);
+  return launch_rows(h, a, in->dtype, ebk::kModeScore, entropies != nullptr, false, false,
+                     (cudaStream_t)stream);
 }
 
 int eb_token_logprobs_backward(eb_scorer_t* h, const eb_score_input_t* in,
@@ -222,7 +324,8 @@ int eb_token_logprobs_backward(eb_scorer_t* h, const eb_score_input_t* in,
   a.ldd = ldd;
   a.g_lp = d_logprobs;
   a.g_h = d_entropies;
-  return launch_rows(h, a, in->dtype, ebk::kModeGrad, false, (cudaStream_t)stream);
+  return launch_rows(h, a, in->dtype, ebk::kModeGrad, d_entropies != nullptr, true, false,
+                     (cudaStream_t)stream);
 }
 
 int eb_policy_loss(eb_scorer_t* h, const eb_score_input_t* in, const eb_policy_t* p, float* terms,
@@ -255,7 +358,8 @@ int eb_policy_loss(eb_scorer_t* h, const eb_score_input_t* in, const eb_policy_t
   a.ent_coef = (float)p->entropy_coef;
   a.scale = p->scale;
   a.terms = terms;
-  return launch_rows(h, a, in->dtype, ebk::kModePolicy, false, (cudaStream_t)stream);
+  return launch_rows(h, a, in->dtype, ebk::kModePolicy, true, d_logits != nullptr, false,
+                     (cudaStream_t)stream);
 }
 
 int eb_preference_loss(eb_scorer_t* h, const eb_score_input_t* in, const eb_preference_t* p,
@@ -280,7 +384,7 @@ int eb_preference_loss(eb_scorer_t* h, const eb_score_input_t* in, const eb_pref
   a.n_off = 2 * p->pairs;
   a.logprobs = logprobs ? logprobs : h->lp;
   if (in->rows > 0 &&
-      (rc = launch_rows(h, a, in->dtype, ebk::kModeScore, false, st)) != EB_OK)
+      (rc = launch_rows(h, a, in->dtype, ebk::kModeScore, false, false, false, st)) != EB_OK)
     return rc;
   if (p->pairs == 0) {
     if (cudaMemsetAsync(loss, 0, sizeof(float), st) != cudaSuccess) return EB_ERR_CUDA;
@@ -311,7 +415,7 @@ int eb_preference_loss(eb_scorer_t* h, const eb_score_input_t* in, const eb_pref
   a.d_logits = d_logits;
   a.ldd = ldd;
   a.g_lp = h->g;
-  return launch_rows(h, a, in->dtype, ebk::kModeGrad, true, st);
+  return launch_rows(h, a, in->dtype, ebk::kModeGrad, false, true, true, st);
 }
 
 int eb_lmhead_logprobs(eb_scorer_t* h, const void* hidden, const void* weight, int32_t rows,

@@ -66,6 +66,7 @@ struct ScoreArgs {
   float* terms;            // kModePolicy: [kPolicyTerms]
   uint32_t* counter;       // arrivals of the grid, zero between launches
   uint32_t* status;
+  uint64_t wait_ns;
 };
 
 template <int DT>
@@ -169,30 +170,7 @@ __device__ __forceinline__ RowResult row_result(RowSums s, float za, float c2) {
   return r;
 }
 
-// Per-row inputs, read once per row.
-struct RowIn {
-  int token;
-  bool live;  // counts: token >= 0, weight not 0, inside the sequences
-  bool bad;   // token >= V
-  float T, c2, iT, weight;
-};
-
 __device__ __forceinline__ bool row_temp_ok(float T) { return T > 0.f && T < INFINITY; }
-
-__device__ __forceinline__ RowIn row_in(const ScoreArgs& p, int row) {
-  RowIn r;
-  r.token = p.tokens[row];
-  r.weight = p.weights ? p.weights[row] : 1.f;
-  r.live = r.token >= 0 && r.weight != 0.f;
-  if (p.offsets) r.live = r.live && row >= p.offsets[0] && row < p.offsets[p.n_off];
-  r.bad = r.token >= p.V;
-  r.T = p.temps ? p.temps[row] : p.temp;
-  // a temperature that is not finite and positive gives a row of NaN
-  if (!row_temp_ok(r.T)) r.T = __int_as_float(0x7fc00000);
-  r.c2 = kLog2e / r.T;
-  r.iT = 1.f / r.T;
-  return r;
-}
 
 struct RowCoef {
   float g, h;  // upstream gradients of log p_a and H
@@ -201,39 +179,41 @@ struct RowCoef {
 // The policy loss of a row: its gradients, and its terms added to t.
 //   L = w [ max(-A r, -A clip(r)) + k KL - c H ],  r = exp(log p_a - old),
 //   KL = exp(ref - log p_a) - 1 - (ref - log p_a)
-__device__ __forceinline__ RowCoef policy_row(const ScoreArgs& p, int row, const RowResult& r,
-                                              float weight, double (&t)[kPolicyTerms]) {
-  const double w = (double)weight * p.scale;
-  const float A = p.adv[row];
-  const float ratio = expf(r.lp - p.old_lp[row]);
-  const float free = -A * ratio;
+__device__ __forceinline__ RowCoef policy_row(const ScoreArgs& p, const RowResult& r, float weight,
+                                              float old_lp, float adv, float ref_lp, bool count,
+                                              double (&t)[kPolicyTerms]) {
+  const float ratio = expf(r.lp - old_lp);
+  const float free = -adv * ratio;
   // the comparisons keep a NaN ratio NaN
   const float held_ratio = ratio < p.clip_lo ? p.clip_lo : ratio > p.clip_hi ? p.clip_hi : ratio;
-  const float held = -A * held_ratio;
+  const float held = -adv * held_ratio;
   const bool cut = held > free;
   float kl = 0.f, dkl = 0.f;
   if (p.ref_lp) {
-    const float gap = p.ref_lp[row] - r.lp;
+    const float gap = ref_lp - r.lp;
     const float back = expm1f(gap);
     kl = back - gap;
     dkl = -back;
   }
-  const float pg = cut ? held : free;
-  const float H = r.H;
-  t[0] += w * ((double)pg + (double)p.kl_coef * kl - (double)p.ent_coef * H);
-  t[1] += w * pg;
-  t[2] += w * kl;
-  t[3] += w * H;
-  t[4] += cut ? w : 0.0;
+  if (count) {
+    const double w = (double)weight * p.scale, pg = cut ? held : free;
+    t[0] += w * (pg + (double)p.kl_coef * kl - (double)p.ent_coef * r.H);
+    t[1] += w * pg;
+    t[2] += w * kl;
+    t[3] += w * r.H;
+    t[4] += cut ? w : 0.0;
+  }
+  const float w = weight * (float)p.scale;
   RowCoef c;
-  c.g = (float)(w * ((cut ? 0.0 : (double)free) + (double)p.kl_coef * dkl));
-  c.h = (float)(-w * (double)p.ent_coef);
+  c.g = w * fmaf(p.kl_coef, dkl, cut ? 0.f : free);
+  c.h = -w * p.ent_coef;
   return c;
 }
 
-// The last CTA of the grid sums the CTAs' terms in CTA order (the same order
-// at every launch of one grid).  Called by one whole block, after its own
-// thread 0 wrote part[blockIdx.x].
+// The last of n CTAs to arrive sums the parts, in an order of its own that
+// does not depend on who arrived when: the same bits at every launch of one
+// grid.  Called by one whole block each, after its part was written.
+template <int NW>
 __device__ __forceinline__ void policy_total(const ScoreArgs& p, int n) {
   __shared__ int last;
   if (threadIdx.x == 0) {
@@ -243,96 +223,638 @@ __device__ __forceinline__ void policy_total(const ScoreArgs& p, int n) {
   }
   __syncthreads();
   if (!last) return;
-  if (threadIdx.x < kPolicyTerms) {
+  const int lane = threadIdx.x & 31;
+  for (int k = threadIdx.x >> 5; k < kPolicyTerms; k += NW + 1) {
     double s = 0.0;
-    for (int i = 0; i < n; ++i) s += __ldcg(p.part + (size_t)i * kPolicyTerms + threadIdx.x);
-    p.terms[threadIdx.x] = (float)s;
+    for (int i = lane; i < n; i += 32) s += __ldcg(p.part + (size_t)i * kPolicyTerms + k);
+    for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    if (lane == 0) p.terms[k] = (float)s;
   }
 }
 
 // ---------------------------------------------------------------------------
-// One block per row
+// Rows on thread-block clusters
+//
+// A cluster of C CTAs takes one row at a time; CTA c holds the c-th share of
+// it.  A producer warp copies the share into a ring of 8 KB stages (bulk
+// copies); the consumer warps fold each stage into a running (reference,
+// sum e, sum e d).  Every consumer warp sends its sums to every CTA of the
+// cluster (st.async into distributed shared memory, counted by an mbarrier),
+// and each warp joins all of them itself: one hop, no block barrier, the same
+// bits in every CTA.  For a gradient the stages are kept until then, and the
+// same threads turn the row they hold into its gradient: the logits are read
+// from HBM once.  Freed stages take the next row at once, so its copy runs
+// under this row's second half.  A share longer than the ring (resident = 0)
+// is copied a second time instead.
+//
+// Rows start at any element.  A share is a range of 16-byte granules of the
+// row's 16-byte-aligned image; the granules that the row fills only partly
+// (at its two ends) are gathered element by element, with -inf in the places
+// that are not the row's, and stored element by element.
 // ---------------------------------------------------------------------------
-constexpr int kRowThreads = 512;
+constexpr int kStageBytes = 8192;
+constexpr int kStageGran = kStageBytes / 16;
+constexpr int kMaxCluster = 16;
+// A thread moves its reference only when a logit exceeds it by 2^kLazy: the
+// sums are relative to any nearby value as exactly as to the maximum.
+constexpr float kLazy = 8.0f;
+
+struct RingArgs {
+  int mode, reverse;
+  int C;         // CTAs per cluster
+  int stages;    // of the ring
+  int resident;  // a share fits the ring: copied once
+};
+
+__host__ __device__ constexpr size_t ring_smem(int stages, int warps) {
+  return (size_t)stages * kStageBytes + (size_t)2 * kMaxCluster * warps * 16 +
+         (size_t)(2 * stages + 2) * 8 + 16;
+}
+
+// -- packed fp32 pairs --------------------------------------------------------
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf2_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf2_min(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// -- clusters -------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t smem_addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_async4(uint32_t addr, float a, float b, float c, float d,
+                                          uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, "
+      "[%5];" ::"r"(addr),
+      "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(__float_as_uint(c)),
+      "r"(__float_as_uint(d)), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// One granule of 16 bytes as packed fp32 pairs.
+template <int DT>
+struct Granule {
+  static constexpr int kPairs = ScoreType<DT>::kPer16 / 2;
+  uint64_t v[kPairs];
+};
+template <int DT>
+__device__ __forceinline__ Granule<DT> granule(const uint4& w) {
+  Granule<DT> g;
+  if constexpr (DT == kScoreF32) {
+    g.v[0] = pack2(__uint_as_float(w.x), __uint_as_float(w.y));
+    g.v[1] = pack2(__uint_as_float(w.z), __uint_as_float(w.w));
+  } else {
+    g.v[0] = pack2(bf_lo(w.x), bf_hi(w.x));
+    g.v[1] = pack2(bf_lo(w.y), bf_hi(w.y));
+    g.v[2] = pack2(bf_lo(w.z), bf_hi(w.z));
+    g.v[3] = pack2(bf_lo(w.w), bf_hi(w.w));
+  }
+  return g;
+}
+
+// Element i of a granule set to -inf.
+template <int DT>
+__device__ __forceinline__ void granule_drop(uint4& w, int i) {
+  uint32_t* x = &w.x;
+  if constexpr (DT == kScoreF32) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k == i) x[k] = 0xff800000u;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k == (i >> 1))
+        x[k] = (i & 1) ? (x[k] & 0xffffu) | 0xff800000u : (x[k] & 0xffff0000u) | 0xff80u;
+  }
+}
+
+// Largest and smallest element of N granules (NaN is passed over: it shows in
+// the sums).
+template <int DT, int N>
+__device__ __forceinline__ void granule_range(const uint4 (&w)[N], float& hi, float& lo) {
+  if constexpr (DT == kScoreF32) {
+    float a = __uint_as_float(w[0].x), b = a;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const float x[4] = {__uint_as_float(w[n].x), __uint_as_float(w[n].y),
+                          __uint_as_float(w[n].z), __uint_as_float(w[n].w)};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        a = fmaxf(a, x[k]);
+        b = fminf(b, x[k]);
+      }
+    }
+    hi = a;
+    lo = b;
+  } else {
+    uint32_t a = w[0].x, b = a;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      a = bf2_max(bf2_max(bf2_max(a, w[n].x), bf2_max(w[n].y, w[n].z)), w[n].w);
+      b = bf2_min(bf2_min(bf2_min(b, w[n].x), bf2_min(w[n].y, w[n].z)), w[n].w);
+    }
+    hi = fmaxf(bf_lo(a), bf_hi(a));
+    lo = fminf(bf_lo(b), bf_hi(b));
+  }
+}
+
+// A thread's running sums: pairs, two chains each.
+struct ThreadSums {
+  float m;
+  uint64_t R[2], Q[2];
+};
+
+template <int DT, bool ENT, int N>
+__device__ __forceinline__ void fold(ThreadSums& s, const uint4 (&w)[N], float c2, bool& deep) {
+  float hi, lo;
+  granule_range<DT, N>(w, hi, lo);
+  if ((hi - s.m) * c2 > kLazy) {  // also from the empty reference -FLT_MAX
+    const float d = fmaxf((s.m - hi) * c2, -kDeep), f = ex2(d);
+    const uint64_t f2 = pack2(f, f), d2 = pack2(d, d);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      s.Q[k] = mul2(f2, fma2(d2, s.R[k], s.Q[k]));
+      s.R[k] = mul2(f2, s.R[k]);
+    }
+    s.m = hi;
+  }
+  const uint64_t nm = pack2(-s.m, -s.m), cc = pack2(c2, c2);
+  const bool clamp = ENT && (lo - s.m) * c2 < -kDeep;
+  if (clamp) deep = true;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const Granule<DT> g = granule<DT>(w[n]);
+#pragma unroll
+    for (int k = 0; k < Granule<DT>::kPairs; ++k) {
+      uint64_t d = mul2(add2(g.v[k], nm), cc);
+      float d0, d1;
+      unpack2(d, d0, d1);
+      if (ENT && clamp) {
+        d0 = d0 < -kDeep ? -kDeep : d0;
+        d1 = d1 < -kDeep ? -kDeep : d1;
+        d = pack2(d0, d1);
+      }
+      const uint64_t e = pack2(ex2(d0), ex2(d1));
+      s.R[k & 1] = add2(s.R[k & 1], e);
+      if (ENT) s.Q[k & 1] = fma2(e, d, s.Q[k & 1]);
+    }
+  }
+}
+
+__device__ __forceinline__ float pair_sum(const uint64_t (&v)[2]) {
+  float a, b;
+  unpack2(add2(v[0], v[1]), a, b);
+  return a + b;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// The warp's parts joined in every lane.
+__device__ __forceinline__ RowSums warp_join(RowSums s, float c2) {
+  const float m = warp_max(s.m);
+  const float d = fmaxf((s.m - m) * c2, -kDeep), f = ex2(d);
+  float Q = f * fmaf(d, s.R, s.Q), R = s.R * f;
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) {
+    R += __shfl_xor_sync(0xffffffffu, R, k);
+    Q += __shfl_xor_sync(0xffffffffu, Q, k);
+  }
+  return RowSums{m, R, Q};
+}
+
+// A CTA's share of a row.
+struct RowShare {
+  int64_t base;  // byte offset of the row's aligned image from the buffer's start (may be < 0)
+  int shift;     // elements of the image before the row
+  int g0, n;     // first granule, granules
+  int whole0, whole1;  // granules of the image that lie inside the row: [whole0, whole1)
+};
 
 template <int DT>
-__global__ void __launch_bounds__(kRowThreads)
-    score_rows_kernel(const ScoreArgs p, const int mode, const bool reverse) {
-  constexpr int kB = ScoreType<DT>::kBytes;
-  __shared__ RowSums warp_sums[kRowThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  double t[kPolicyTerms] = {};
-  for (int i = blockIdx.x; i < p.rows; i += gridDim.x) {
-    const int row = reverse ? p.rows - 1 - i : i;
-    const RowIn in = row_in(p, row);
-    const char* z = static_cast<const char*>(p.logits) + (size_t)row * (size_t)p.ld * kB;
-    char* dz = p.d_logits ? static_cast<char*>(p.d_logits) + (size_t)row * (size_t)p.ldd * kB
-                          : nullptr;
-    if (!in.live) {
-      if (tid == 0) {
-        if (p.logprobs) p.logprobs[row] = 0.f;
-        if (p.entropies) p.entropies[row] = 0.f;
+__device__ __forceinline__ RowShare row_share(const void* buf, int64_t ld, int row, int V, int C,
+                                              int rank) {
+  constexpr int kB = ScoreType<DT>::kBytes, kPer = ScoreType<DT>::kPer16;
+  RowShare s;
+  const int64_t off = (int64_t)row * ld * kB;
+  const int mis = (int)(((uintptr_t)buf + (uintptr_t)off) & 15u);
+  s.base = off - mis;
+  s.shift = mis / kB;
+  const int end = s.shift + V;
+  const int G = (end + kPer - 1) / kPer;
+  const int per = ((G + C - 1) / C + 7) & ~7;
+  s.g0 = min(G, rank * per);
+  s.n = min(G - s.g0, per);
+  s.whole0 = s.shift ? 1 : 0;
+  s.whole1 = end / kPer;
+  return s;
+}
+
+template <int DT, bool ENT, bool GRAD, int NW>
+__global__ void __launch_bounds__((NW + 1) * 32, NW == 8 ? 2 : 6)
+    score_ring_kernel(const ScoreArgs p, const RingArgs q) {
+  constexpr int kB = ScoreType<DT>::kBytes, kPer = ScoreType<DT>::kPer16;
+  constexpr int kT = NW * 32;
+  constexpr int kIter = kStageGran / kT;  // granules of a stage per thread
+  constexpr int kN = 2;                   // granules folded at a time
+  static_assert(kIter % kN == 0, "a stage is a whole number of folds");
+  extern __shared__ __align__(128) unsigned char ring[];
+  float4* part = reinterpret_cast<float4*>(ring + (size_t)q.stages * kStageBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(part + 2 * kMaxCluster * NW);
+  uint64_t* empty = full + q.stages;
+  uint64_t* rowbar = empty + q.stages;  // [2]
+  int* abort_flag = reinterpret_cast<int*>(rowbar + 2);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = q.C;
+  const int rank = (int)cluster_rank();
+  const int cid = blockIdx.x / C, ncl = gridDim.x / C;
+  if (tid == 0) {
+    for (int s = 0; s < q.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], NW);
+    }
+    mbar_init(&rowbar[0], 1);
+    mbar_init(&rowbar[1], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  cluster_sync_all();
+
+  int row_lo = 0, row_hi = p.rows;
+  if (p.offsets) {
+    row_lo = p.offsets[0];
+    row_hi = p.offsets[p.n_off];
+  }
+  auto row_of = [&](int i) { return q.reverse ? p.rows - 1 - i : i; };
+  auto live = [&](int row, int token, float weight) {
+    return token >= 0 && weight != 0.f && row >= row_lo && row < row_hi;
+  };
+  auto fail = [&]() {
+    atomicOr(p.status, kScoreTimeout);
+    *(volatile int*)abort_flag = 1;
+  };
+  bool ok = true;
+
+  if (warp == NW) {
+    // ------------------------------------------------------------ producer
+    const uint64_t once = evict_first_policy();
+    int issued = 0, slot = 0;
+    uint32_t phase = 1;  // the parity of an empty stage's first wait: passes at once
+    int i = cid;
+    int token = -1;
+    float weight = 1.f;
+    if (i < p.rows) {
+      token = p.tokens[row_of(i)];
+      if (p.weights) weight = p.weights[row_of(i)];
+    }
+    for (; i < p.rows && ok; i += ncl) {
+      const int row = row_of(i);
+      const bool on = live(row, token, weight);
+      if (i + ncl < p.rows) {
+        token = p.tokens[row_of(i + ncl)];
+        if (p.weights) weight = p.weights[row_of(i + ncl)];
       }
-      if (dz)
-        for (int v = tid; v < p.V; v += kRowThreads) store_grad<DT>(dz, v, 0.f);
-      continue;
+      if (!on) continue;
+      const RowShare s = row_share<DT>(p.logits, p.ld, row, p.V, C, rank);
+      const char* img = static_cast<const char*>(p.logits) + s.base;
+      const int copies = GRAD && !q.resident ? 2 : 1;
+      for (int c = 0; c < copies && ok; ++c) {
+        for (int g = s.g0; g < s.g0 + s.n; g += kStageGran) {
+          // one lane waits, the warp goes on together
+          bool free = true;
+          if (lane == 0) free = mbar_wait(&empty[slot], phase, p.wait_ns, abort_flag);
+          if (!__all_sync(0xffffffffu, free)) {
+            ok = false;
+            break;
+          }
+          unsigned char* dst = ring + (size_t)slot * kStageBytes;
+          const int end = min(g + kStageGran, s.g0 + s.n);
+          const int b0 = max(g, s.whole0), b1 = max(b0, min(end, s.whole1));
+          if (b0 != g || b1 != end) {
+            // granules the row fills in part: at most the first and the last
+            for (int e = lane; e < 2 * kPer; e += 32) {
+              const int gr = e < kPer ? 0 : s.whole1;
+              const bool mine = gr >= g && gr < end && (gr < b0 || gr >= b1) &&
+                                (e < kPer || s.whole1 != 0 || s.whole0 == 0);
+              const int at = gr * kPer + (e & (kPer - 1));  // element of the image
+              if (mine) {
+                const int v = at - s.shift;
+                const bool in = v >= 0 && v < p.V;
+                unsigned char* to = dst + (size_t)(gr - g) * 16 + (e & (kPer - 1)) * kB;
+                if (kB == 4)
+                  *reinterpret_cast<uint32_t*>(to) =
+                      in ? reinterpret_cast<const uint32_t*>(img)[at] : 0xff800000u;
+                else
+                  *reinterpret_cast<uint16_t*>(to) =
+                      in ? reinterpret_cast<const uint16_t*>(img)[at] : (uint16_t)0xff80u;
+              }
+            }
+            __syncwarp();
+          }
+          if (lane == 0) {
+            const uint32_t bytes = (uint32_t)(b1 - b0) * 16u;
+            mbar_arrive_expect_tx(&full[slot], bytes);
+            if (bytes)
+              bulk_load(dst + (size_t)(b0 - g) * 16, img + (size_t)b0 * 16, bytes, &full[slot],
+                        once);
+          }
+          ++issued;
+          if (++slot == q.stages) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
     }
-    const float za = in.bad ? __int_as_float(0x7fc00000) : load_logit<DT>(z, in.token);
-    RowSums s = row_sums_empty();
-    for (int v = tid; v < p.V; v += kRowThreads) {
-      if (v == in.token) continue;
-      const float x = load_logit<DT>(z, v);
-      if (x > s.m) s = row_sums_join(s, RowSums{x, 0.f, 0.f}, in.c2);
-      // a NaN logit stays NaN through the clamp's comparison
-      float d = (x - s.m) * in.c2;
-      d = d < -kDeep ? -kDeep : d;
-      const float e = ex2(d);
-      s.R += e;
-      s.Q = fmaf(e, d, s.Q);
+    if (!ok && lane == 0) fail();
+    // every copy issued has landed before the CTA may leave
+    if (lane == 0)
+      for (int k = max(0, issued - q.stages); k < issued; ++k)
+        mbar_wait(&full[k % q.stages], (uint32_t)(k / q.stages) & 1u, kDrainLimitNs);
+    __syncwarp();
+  } else {
+    // ----------------------------------------------------------- consumers
+    double t[kPolicyTerms] = {};
+    const bool writer = rank == 0 && warp == 0 && lane == 0;
+    int slot = 0;
+    uint32_t phase = 0;
+    uint32_t count = 0;  // rows exchanged
+    int i = cid;
+    int token = -1;
+    float weight = 1.f, T = p.temp;
+    if (i < p.rows) {
+      token = p.tokens[row_of(i)];
+      if (p.weights) weight = p.weights[row_of(i)];
+      if (p.temps) T = p.temps[row_of(i)];
     }
-    for (int k = 16; k > 0; k >>= 1) s = row_sums_shuffle(s, k, in.c2);
-    __syncthreads();
-    if (lane == 0) warp_sums[warp] = s;
-    __syncthreads();
-    s = warp_sums[lane % (kRowThreads / 32)];
-    for (int k = 8; k > 0; k >>= 1) s = row_sums_shuffle(s, k, in.c2);
-    const RowResult r = row_result(s, za, in.c2);
-    RowCoef c{0.f, 0.f};
-    if (mode == kModePolicy) {
-      c = policy_row(p, row, r, in.weight, t);
-    } else if (mode == kModeGrad) {
-      c.g = p.g_lp[row];
-      c.h = p.g_h ? p.g_h[row] : 0.f;
-    }
-    if (tid == 0) {
-      if (p.logprobs) p.logprobs[row] = r.lp;
-      if (p.entropies) p.entropies[row] = r.H;
-      const uint32_t bits = (in.bad ? kScoreBadToken : 0u) | (r.finite ? 0u : kScoreNonFinite);
-      if (bits) atomicOr(p.status, bits);
-    }
-    if (dz) {
-      const float a0 = -in.iT * fmaf(c.h, r.H, c.g), a1 = -in.iT * c.h * kLn2;
+    for (; i < p.rows && ok; i += ncl) {
+      const int row = row_of(i);
+      const int a = token;
+      const float wt = weight;
+      const float Trow = row_temp_ok(T) ? T : __int_as_float(0x7fc00000);
+      if (i + ncl < p.rows) {
+        token = p.tokens[row_of(i + ncl)];
+        if (p.weights) weight = p.weights[row_of(i + ncl)];
+        if (p.temps) T = p.temps[row_of(i + ncl)];
+      }
+      const RowShare sh = row_share<DT>(p.logits, p.ld, row, p.V, C, rank);
+      char* dz = nullptr;  // the gradient's image, aligned as the logits' (or element by element)
+      bool dz_vec = false;
+      if (GRAD) {
+        char* d = static_cast<char*>(p.d_logits) + (int64_t)row * p.ldd * kB;
+        dz = d - sh.shift * kB;
+        dz_vec = ((uintptr_t)dz & 15u) == 0;
+      }
+      // the gradient's granule g: whole and aligned, or element by element
+      auto put = [&](int g, const uint4& w) {
+        if (dz_vec && g >= sh.whole0 && g < sh.whole1) {
+          *reinterpret_cast<uint4*>(dz + (int64_t)g * 16) = w;
+        } else {
+          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            const int v = g * kPer + k - sh.shift;
+            if (v < 0 || v >= p.V) continue;
+            if (kB == 4)
+              reinterpret_cast<uint32_t*>(dz)[(int64_t)g * kPer + k] = x[k & 3];
+            else
+              reinterpret_cast<uint16_t*>(dz)[(int64_t)g * kPer + k] =
+                  (uint16_t)(x[(k >> 1) & 3] >> (16 * (k & 1)));
+          }
+        }
+      };
+      if (!live(row, a, wt)) {
+        if (writer) {
+          if (p.logprobs) p.logprobs[row] = 0.f;
+          if (p.entropies) p.entropies[row] = 0.f;
+        }
+        if (GRAD)
+          for (int g = sh.g0 + tid; g < sh.g0 + sh.n; g += kT) put(g, make_uint4(0, 0, 0, 0));
+        continue;
+      }
+      const bool bad = a >= p.V;
+      const float za = bad ? __int_as_float(0x7fc00000)
+                           : load_logit<DT>(static_cast<const char*>(p.logits) +
+                                                (int64_t)row * p.ld * kB, a);
+      float x0 = 0.f, x1 = 0.f, x2 = 0.f;  // the mode's own inputs
+      if (q.mode == kModePolicy) {
+        x0 = p.old_lp[row];
+        x1 = p.adv[row];
+        if (p.ref_lp) x2 = p.ref_lp[row];
+      } else if (q.mode == kModeGrad) {
+        x0 = p.g_lp[row];
+        if (p.g_h) x1 = p.g_h[row];
+      }
+      const float c2 = kLog2e / Trow;
+      uint64_t* bar = &rowbar[count & 1u];
+      if (tid == 0) mbar_arrive_expect_tx(bar, (uint32_t)(C * NW * 16));
+
+      // the token's place: this thread's granule `mine` (counted along its own
+      // granules), element `el`
+      int mine = -1;
+      const int at = a + sh.shift, ag = at / kPer - sh.g0, el = at & (kPer - 1);
+      if (!bad && ag >= 0 && ag < sh.n && (ag & (kT - 1)) == tid) mine = ag / kT;
+
+      // pass 1: the sums
+      ThreadSums s;
+      s.m = -FLT_MAX;
+      s.R[0] = s.R[1] = s.Q[0] = s.Q[1] = 0ull;
+      bool deep = false;
+      const int slot0 = slot;
+      int n = sh.n;  // granules left
+      int it = 0;
+      while (n > 0) {
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(&full[slot], phase, p.wait_ns, abort_flag))) {
+          ok = false;
+          break;
+        }
+        const uint4* st = reinterpret_cast<const uint4*>(ring + (size_t)slot * kStageBytes);
+#pragma unroll
+        for (int j = 0; j < kIter; j += kN) {
+          if (j * kT + tid >= n) break;
+          uint4 w[kN];
+#pragma unroll
+          for (int k = 0; k < kN; ++k) {
+            const int g = (j + k) * kT + tid;
+            if (g < n)
+              w[k] = st[g];
+            else  // past the share: nothing
+              w[k] = kB == 4 ? make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u)
+                             : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+            if (it + j + k == mine) granule_drop<DT>(w[k], el);
+          }
+          fold<DT, ENT, kN>(s, w, c2, deep);
+        }
+        if (!GRAD || !q.resident) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[slot]);
+        }
+        it += kIter;
+        n -= kStageGran;
+        if (++slot == q.stages) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      // this warp's sums to every CTA of the cluster (the token's logit rides
+      // along: it has been read before any CTA may overwrite the row)
+      RowSums rs = warp_join(RowSums{s.m, pair_sum(s.R), ENT ? pair_sum(s.Q) : 0.f}, c2);
+      if (lane < C) {
+        const uint32_t to = smem_u32(&part[(count & 1u) * kMaxCluster * NW + rank * NW + warp]);
+        st_async4(map_rank(to, lane), rs.m, rs.R, rs.Q, za, map_rank(smem_u32(bar), lane));
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(bar, (count >> 1) & 1u, p.wait_ns, abort_flag))) {
+        ok = false;
+        break;
+      }
+      RowSums all = row_sums_empty();
+      for (int k = lane; k < C * NW; k += 32) {
+        const float4 v = part[(count & 1u) * kMaxCluster * NW + k];
+        all = row_sums_join(all, RowSums{v.x, v.y, v.z}, c2);
+      }
+      all = warp_join(all, c2);
+      ++count;
+      const RowResult r = row_result(all, za, c2);
+      RowCoef c{0.f, 0.f};
+      if (q.mode == kModePolicy) {
+        c = policy_row(p, r, wt, x0, x1, x2, writer, t);
+      } else {
+        c.g = x0;
+        c.h = x1;
+      }
+      if (writer) {
+        if (p.logprobs) p.logprobs[row] = r.lp;
+        if (ENT && p.entropies) p.entropies[row] = r.H;
+        const uint32_t bits = (bad ? kScoreBadToken : 0u) | (r.finite ? 0u : kScoreNonFinite);
+        if (bits) atomicOr(p.status, bits);
+      }
+      if (!GRAD) continue;
+
+      // pass 2: the gradient, from the stages that still hold the row
+      const float iT = 1.f / Trow;
+      const float a0 = -iT * (ENT ? fmaf(c.h, r.H, c.g) : c.g), a1 = -iT * c.h * kLn2;
       // p_a = 0: log p_a may be -inf, its entropy term is 0
-      const float ha = r.pa > 0.f ? c.h * r.pa * (r.lp + r.H) : r.pa;
-      const float at = in.iT * (c.g * r.rest - ha);
-      const bool ent = c.h != 0.f;
-      for (int v = tid; v < p.V; v += kRowThreads) {
-        float d = (load_logit<DT>(z, v) - r.M) * in.c2;
-        d = d < -kDeep ? -kDeep : d;
-        const float x = d - r.l2S;
-        const float pv = ex2(x);
-        float dv = pv * (ent ? fmaf(a1, x, a0) : a0);
-        if (v == in.token) dv = at;
-        store_grad<DT>(dz, v, dv);
+      const float ha = !ENT ? 0.f : r.pa > 0.f ? c.h * r.pa * (r.lp + r.H) : r.pa;
+      const float own = iT * (c.g * r.rest - ha);
+      const uint64_t nM = pack2(-r.M, -r.M), cc = pack2(c2, c2), nl = pack2(-r.l2S, -r.l2S),
+                     A0 = pack2(a0, a0), A1 = pack2(a1, a1);
+      if (ENT && (s.m - r.M) * c2 < -kDeep) deep = true;
+      if (q.resident) slot = slot0;
+      n = sh.n;
+      it = 0;
+      int g = sh.g0 + tid;
+      while (n > 0) {
+        if (!q.resident &&
+            !__all_sync(0xffffffffu, mbar_wait(&full[slot], phase, p.wait_ns, abort_flag))) {
+          ok = false;
+          break;
+        }
+        const uint4* st = reinterpret_cast<const uint4*>(ring + (size_t)slot * kStageBytes);
+#pragma unroll
+        for (int j = 0; j < kIter; ++j, g += kT) {
+          if (j * kT + tid >= n) continue;
+          const Granule<DT> z = granule<DT>(st[j * kT + tid]);
+          float o[kPer];
+#pragma unroll
+          for (int k = 0; k < kPer / 2; ++k) {
+            uint64_t x = fma2(add2(z.v[k], nM), cc, nl);
+            float xa, xb;
+            unpack2(x, xa, xb);
+            if (ENT && deep) {
+              xa = xa < -kDeep ? -kDeep : xa;
+              xb = xb < -kDeep ? -kDeep : xb;
+              x = pack2(xa, xb);
+            }
+            const uint64_t e = pack2(ex2(xa), ex2(xb));
+            unpack2(mul2(e, ENT ? fma2(A1, x, A0) : A0), o[2 * k], o[2 * k + 1]);
+          }
+          if (it + j == mine) {
+#pragma unroll
+            for (int k = 0; k < kPer; ++k)
+              if (k == el) o[k] = own;
+          }
+          uint4 w;
+          if constexpr (DT == kScoreF32)
+            w = make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]),
+                           __float_as_uint(o[3]));
+          else
+            w = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
+                           pack_bf16(o[6], o[7]));
+          put(g, w);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[slot]);
+        it += kIter;
+        n -= kStageGran;
+        if (++slot == q.stages) {
+          slot = 0;
+          if (!q.resident) phase ^= 1u;
+        }
       }
     }
-  }
-  if (mode == kModePolicy) {
-    if (tid == 0)
+    if (!ok) {
+      if (lane == 0) fail();
+      // sums of this row may still be on their way to other CTAs: they land
+      // well within this pause, before the barrier lets any CTA leave
+      __nanosleep(100000);
+      __syncwarp();
+    }
+    if (q.mode == kModePolicy && writer)
       for (int k = 0; k < kPolicyTerms; ++k)
-        p.part[(size_t)blockIdx.x * kPolicyTerms + k] = t[k];
-    policy_total(p, gridDim.x);
+        p.part[(size_t)cid * kPolicyTerms + k] = ok ? t[k] : (double)__int_as_float(0x7fc00000);
   }
+  __syncthreads();
+  cluster_sync_all();
+  if (q.mode == kModePolicy && rank == 0) policy_total<NW>(p, ncl);
 }
 
 // ---------------------------------------------------------------------------
