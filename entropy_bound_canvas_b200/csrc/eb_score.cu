@@ -46,14 +46,14 @@ int ring_variant(bool bf16, bool ent, bool grad, bool wide) {
   return (bf16 ? 8 : 0) + (ent ? 4 : 0) + (grad ? 2 : 0) + (wide ? 1 : 0);
 }
 
-// Two wide CTAs (13 stages, 104 KB) or six narrow ones (4 stages, 32 KB)
+// Two wide CTAs (6 stages of 16 KB) or four narrow ones (4 stages of 8 KB)
 // share an SM.
-constexpr int kWideStages = 13, kNarrowStages = 4;
+constexpr int kWideStages = 6, kNarrowStages = 4;
 size_t ring_smem_of(bool wide) {
-  return wide ? ebk::ring_smem(kWideStages, 8) : ebk::ring_smem(kNarrowStages, 4);
+  return wide ? ebk::ring_layout(kWideStages, 8).total : ebk::ring_layout(kNarrowStages, 4).total;
 }
 constexpr int64_t kNarrowBytes = 16384;  // rows up to this take the narrow form
-constexpr int kShareStages = 8;          // a wide CTA's share where the cluster allows it
+constexpr int kShareStages = 4;          // a wide CTA's share where the cluster allows it
 constexpr int kMaxC = 8;
 
 struct DeviceInfo {
@@ -171,11 +171,12 @@ struct RingPlan {
   int resident;  // a CTA's share of a row fits its ring
 };
 
-int share_stages(int64_t row_bytes, int C) {
+int share_stages(int64_t row_bytes, int C, int warps) {
+  const int gran = ebk::stage_bytes(warps) / 16;
   // the aligned image of a row spans up to one granule more than its bytes
   const int64_t G = (row_bytes + 15) / 16 + 1;
   const int64_t per = ((G + C - 1) / C + 7) / 8 * 8;
-  return (int)std::min<int64_t>((per + ebk::kStageGran - 1) / ebk::kStageGran, 1 << 20);
+  return (int)std::min<int64_t>((per + gran - 1) / gran, 1 << 20);
 }
 
 RingPlan ring_plan(int sms, int64_t rows, int64_t row_bytes) {
@@ -183,11 +184,11 @@ RingPlan ring_plan(int sms, int64_t rows, int64_t row_bytes) {
   r.wide = row_bytes > kNarrowBytes;
   r.C = 1;
   if (r.wide) {
-    while (r.C < kMaxC && share_stages(row_bytes, r.C) > kShareStages) r.C *= 2;
-    while (r.C < kMaxC && rows * r.C * 2 <= 2 * sms && row_bytes / r.C > 2 * ebk::kStageBytes)
+    while (r.C < kMaxC && share_stages(row_bytes, r.C, 8) > kShareStages) r.C *= 2;
+    while (r.C < kMaxC && rows * r.C * 2 <= 2 * sms && row_bytes / r.C > ebk::stage_bytes(8))
       r.C *= 2;
   }
-  r.resident = share_stages(row_bytes, r.C) <= (r.wide ? kWideStages : kNarrowStages);
+  r.resident = share_stages(row_bytes, r.C, r.wide ? 8 : 4) <= (r.wide ? kWideStages : kNarrowStages);
   return r;
 }
 
@@ -204,7 +205,7 @@ int launch_rows(const eb_scorer* h, const ScoreArgs& a, int dtype, int mode, boo
   q.resident = r.resident;
   cudaLaunchConfig_t lc;
   std::memset(&lc, 0, sizeof(lc));
-  lc.blockDim = dim3((warps + 1) * 32);
+  lc.blockDim = dim3((warps + 2) * 32);
   lc.dynamicSmemBytes = ring_smem_of(r.wide);
   lc.stream = st;
   cudaLaunchAttribute attr[1];

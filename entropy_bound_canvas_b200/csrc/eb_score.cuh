@@ -213,7 +213,7 @@ __device__ __forceinline__ RowCoef policy_row(const ScoreArgs& p, const RowResul
 // The last of n CTAs to arrive sums the parts, in an order of its own that
 // does not depend on who arrived when: the same bits at every launch of one
 // grid.  Called by one whole block each, after its part was written.
-template <int NW>
+template <int WARPS>
 __device__ __forceinline__ void policy_total(const ScoreArgs& p, int n) {
   __shared__ int last;
   if (threadIdx.x == 0) {
@@ -224,7 +224,7 @@ __device__ __forceinline__ void policy_total(const ScoreArgs& p, int n) {
   __syncthreads();
   if (!last) return;
   const int lane = threadIdx.x & 31;
-  for (int k = threadIdx.x >> 5; k < kPolicyTerms; k += NW + 1) {
+  for (int k = threadIdx.x >> 5; k < kPolicyTerms; k += WARPS) {
     double s = 0.0;
     for (int i = lane; i < n; i += 32) s += __ldcg(p.part + (size_t)i * kPolicyTerms + k);
     for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
@@ -236,28 +236,34 @@ __device__ __forceinline__ void policy_total(const ScoreArgs& p, int n) {
 // Rows on thread-block clusters
 //
 // A cluster of C CTAs takes one row at a time; CTA c holds the c-th share of
-// it.  A producer warp copies the share into a ring of 8 KB stages (bulk
-// copies); the consumer warps fold each stage into a running (reference,
-// sum e, sum e d).  Every consumer warp sends its sums to every CTA of the
-// cluster (st.async into distributed shared memory, counted by an mbarrier),
-// and each warp joins all of them itself: one hop, no block barrier, the same
-// bits in every CTA.  For a gradient the stages are kept until then, and the
-// same threads turn the row they hold into its gradient: the logits are read
-// from HBM once.  Freed stages take the next row at once, so its copy runs
-// under this row's second half.  A share longer than the ring (resident = 0)
-// is copied a second time instead.
+// it.  Three roles:
+//   producer   (a warp) copies the share into a ring of stages (bulk copies);
+//   consumers  (NW warps) fold each stage into a running (reference, sum e,
+//              sum e d); at the row's end every warp sends its sums into the
+//              finishing CTAs' shared memory (st.async, counted by an
+//              mbarrier);
+//   finisher   (a warp) joins the C NW sums, in an order of its own, and
+//              computes the row's results and its gradient's factors.
+// Without a gradient only the first CTA finishes, and the consumers go on to
+// the next row at once.  With one every CTA does (the same arithmetic, the
+// same bits): the stages are kept until its finisher has the factors, and the
+// same threads turn what they hold into the gradient, so the logits are read
+// from HBM once.  Freed stages take the next row's copy at once.  A share
+// longer than the ring (resident = 0) is copied a second time instead.
 //
 // Rows start at any element.  A share is a range of 16-byte granules of the
 // row's 16-byte-aligned image; the granules that the row fills only partly
 // (at its two ends) are gathered element by element, with -inf in the places
 // that are not the row's, and stored element by element.
 // ---------------------------------------------------------------------------
-constexpr int kStageBytes = 8192;
-constexpr int kStageGran = kStageBytes / 16;
+constexpr int kStageIter = 4;  // granules of a stage per consumer thread
+constexpr __host__ __device__ int stage_bytes(int warps) { return warps * 32 * 16 * kStageIter; }
 constexpr int kMaxCluster = 16;
-// A thread moves its reference only when a logit exceeds it by 2^kLazy: the
-// sums are relative to any nearby value as exactly as to the maximum.
-constexpr float kLazy = 8.0f;
+// A thread moves its reference to a new maximum only when that exceeds it by
+// 2^kLazy: a row that one logit dominates still has that logit as its
+// reference (any other is over 2^kLazy below it), and the others' sums are as
+// exact relative to a nearby value.
+constexpr float kLazy = 2.0f;
 
 struct RingArgs {
   int mode, reverse;
@@ -266,9 +272,24 @@ struct RingArgs {
   int resident;  // a share fits the ring: copied once
 };
 
-__host__ __device__ constexpr size_t ring_smem(int stages, int warps) {
-  return (size_t)stages * kStageBytes + (size_t)2 * kMaxCluster * warps * 16 +
-         (size_t)(2 * stages + 2) * 8 + 16;
+// What the consumers need for a row's gradient.
+struct RowGrad {
+  float M, l2S;  // p = 2^((z - M) c2 - l2S)
+  float a0, a1;  // gradient p (a0 + a1 log2 p)
+  float own;     // the token's element
+};
+
+struct RingLayout {
+  uint32_t part, grad, bars, flag, total;
+};
+__host__ __device__ constexpr RingLayout ring_layout(int stages, int warps) {
+  RingLayout y{};
+  y.part = (uint32_t)(stages * stage_bytes(warps));
+  y.grad = y.part + 2u * kMaxCluster * (uint32_t)warps * 16u;
+  y.bars = y.grad + 2u * 32u;
+  y.flag = y.bars + (2u * (uint32_t)stages + 6u) * 8u;
+  y.total = y.flag + 16u;
+  return y;
 }
 
 // -- packed fp32 pairs --------------------------------------------------------
@@ -300,11 +321,6 @@ __device__ __forceinline__ uint32_t bf2_max(uint32_t a, uint32_t b) {
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t bf2_min(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -327,6 +343,10 @@ __device__ __forceinline__ void st_async4(uint32_t addr, float a, float b, float
       "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(__float_as_uint(c)),
       "r"(__float_as_uint(d)), "r"(bar)
       : "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -354,49 +374,25 @@ __device__ __forceinline__ Granule<DT> granule(const uint4& w) {
   return g;
 }
 
-// Element i of a granule set to -inf.
-template <int DT>
-__device__ __forceinline__ void granule_drop(uint4& w, int i) {
-  uint32_t* x = &w.x;
-  if constexpr (DT == kScoreF32) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k == i) x[k] = 0xff800000u;
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k == (i >> 1))
-        x[k] = (i & 1) ? (x[k] & 0xffffu) | 0xff800000u : (x[k] & 0xffff0000u) | 0xff80u;
-  }
-}
-
-// Largest and smallest element of N granules (NaN is passed over: it shows in
-// the sums).
+// Largest element of N granules (NaN is passed over: it shows in the sums).
 template <int DT, int N>
-__device__ __forceinline__ void granule_range(const uint4 (&w)[N], float& hi, float& lo) {
+__device__ __forceinline__ float granule_max(const uint4 (&w)[N]) {
   if constexpr (DT == kScoreF32) {
-    float a = __uint_as_float(w[0].x), b = a;
+    float a[N];
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const float x[4] = {__uint_as_float(w[n].x), __uint_as_float(w[n].y),
-                          __uint_as_float(w[n].z), __uint_as_float(w[n].w)};
+    for (int n = 0; n < N; ++n)
+      a[n] = fmaxf(fmaxf(__uint_as_float(w[n].x), __uint_as_float(w[n].y)),
+                   fmaxf(__uint_as_float(w[n].z), __uint_as_float(w[n].w)));
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        a = fmaxf(a, x[k]);
-        b = fminf(b, x[k]);
-      }
-    }
-    hi = a;
-    lo = b;
+    for (int n = 1; n < N; ++n) a[0] = fmaxf(a[0], a[n]);
+    return a[0];
   } else {
-    uint32_t a = w[0].x, b = a;
+    uint32_t a[N];
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      a = bf2_max(bf2_max(bf2_max(a, w[n].x), bf2_max(w[n].y, w[n].z)), w[n].w);
-      b = bf2_min(bf2_min(bf2_min(b, w[n].x), bf2_min(w[n].y, w[n].z)), w[n].w);
-    }
-    hi = fmaxf(bf_lo(a), bf_hi(a));
-    lo = fminf(bf_lo(b), bf_hi(b));
+    for (int n = 0; n < N; ++n) a[n] = bf2_max(bf2_max(w[n].x, w[n].y), bf2_max(w[n].z, w[n].w));
+#pragma unroll
+    for (int n = 1; n < N; ++n) a[0] = bf2_max(a[0], a[n]);
+    return fmaxf(bf_lo(a[0]), bf_hi(a[0]));
   }
 }
 
@@ -406,47 +402,83 @@ struct ThreadSums {
   uint64_t R[2], Q[2];
 };
 
+__device__ __forceinline__ float pair_sum(const uint64_t (&v)[2]) {
+  float a, b;
+  unpack2(add2(v[0], v[1]), a, b);
+  return a + b;
+}
+
+// Folds N granules, held in w and at st[k step] in shared memory.  `drop`: the
+// element that is left out (counted through the N granules), or -1; its value
+// goes to `za`.  `deep` is set by elements of whole granules (numbers whole0 ..
+// whole1 - 1, the first one here being g) so far below the reference that
+// their exponent has to be clamped.
 template <int DT, bool ENT, int N>
-__device__ __forceinline__ void fold(ThreadSums& s, const uint4 (&w)[N], float c2, bool& deep) {
-  float hi, lo;
-  granule_range<DT, N>(w, hi, lo);
+__device__ __forceinline__ void fold(ThreadSums& s, const uint4 (&w)[N], const uint4* st, int step,
+                                     int drop, float c2, int g, int whole0, int whole1, float& za,
+                                     bool& deep) {
+  const float hi = granule_max<DT, N>(w);
   if ((hi - s.m) * c2 > kLazy) {  // also from the empty reference -FLT_MAX
     const float d = fmaxf((s.m - hi) * c2, -kDeep), f = ex2(d);
     const uint64_t f2 = pack2(f, f), d2 = pack2(d, d);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      s.Q[k] = mul2(f2, fma2(d2, s.R[k], s.Q[k]));
+      if (ENT) s.Q[k] = mul2(f2, fma2(d2, s.R[k], s.Q[k]));
       s.R[k] = mul2(f2, s.R[k]);
     }
     s.m = hi;
   }
   const uint64_t nm = pack2(-s.m, -s.m), cc = pack2(c2, c2);
-  const bool clamp = ENT && (lo - s.m) * c2 < -kDeep;
-  if (clamp) deep = true;
+  uint64_t R[2] = {0ull, 0ull}, Q[2] = {0ull, 0ull};
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    const Granule<DT> g = granule<DT>(w[n]);
+    const Granule<DT> v = granule<DT>(w[n]);
 #pragma unroll
     for (int k = 0; k < Granule<DT>::kPairs; ++k) {
-      uint64_t d = mul2(add2(g.v[k], nm), cc);
+      const uint64_t d = mul2(add2(v.v[k], nm), cc);
       float d0, d1;
       unpack2(d, d0, d1);
-      if (ENT && clamp) {
-        d0 = d0 < -kDeep ? -kDeep : d0;
-        d1 = d1 < -kDeep ? -kDeep : d1;
-        d = pack2(d0, d1);
-      }
       const uint64_t e = pack2(ex2(d0), ex2(d1));
-      s.R[k & 1] = add2(s.R[k & 1], e);
-      if (ENT) s.Q[k & 1] = fma2(e, d, s.Q[k & 1]);
+      R[k & 1] = add2(R[k & 1], e);
+      if (ENT) Q[k & 1] = fma2(e, d, Q[k & 1]);
     }
   }
-}
-
-__device__ __forceinline__ float pair_sum(const uint64_t (&v)[2]) {
-  float a, b;
-  unpack2(add2(v[0], v[1]), a, b);
-  return a + b;
+  bool again = drop >= 0;
+  if (ENT) {
+    // an exponent of -inf makes e d NaN
+    const float t = pair_sum(Q);
+    again = again || t != t;
+  }
+  if (again) {
+    // rare: element by element, with the clamp and without the dropped one
+    constexpr int kPer = ScoreType<DT>::kPer16;
+    float r1 = 0.f, q1 = 0.f;
+#pragma unroll 1
+    for (int e = 0; e < N * kPer; ++e) {
+      const int off = (e / kPer) * step;
+      const float z = load_logit<DT>(st + off, e % kPer);
+      if (e == drop) {
+        za = z;
+        continue;
+      }
+      float d = (z - s.m) * c2;
+      if (d < -kDeep) {
+        d = -kDeep;
+        if (g + off >= whole0 && g + off < whole1) deep = true;
+      }
+      const float x = ex2(d);
+      r1 += x;
+      q1 = fmaf(x, d, q1);
+    }
+    R[0] = pack2(r1, 0.f);
+    Q[0] = pack2(q1, 0.f);
+    R[1] = Q[1] = 0ull;
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    s.R[k] = add2(s.R[k], R[k]);
+    if (ENT) s.Q[k] = add2(s.Q[k], Q[k]);
+  }
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -495,20 +527,29 @@ __device__ __forceinline__ RowShare row_share(const void* buf, int64_t ld, int r
   return s;
 }
 
+template <int NW>
+struct RingShape {
+  static constexpr int kThreads = (NW + 2) * 32;
+  static constexpr int kCtas = NW == 8 ? 2 : 4;  // per SM
+};
+
 template <int DT, bool ENT, bool GRAD, int NW>
-__global__ void __launch_bounds__((NW + 1) * 32, NW == 8 ? 2 : 6)
+__global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
     score_ring_kernel(const ScoreArgs p, const RingArgs q) {
   constexpr int kB = ScoreType<DT>::kBytes, kPer = ScoreType<DT>::kPer16;
   constexpr int kT = NW * 32;
-  constexpr int kIter = kStageGran / kT;  // granules of a stage per thread
-  constexpr int kN = 2;                   // granules folded at a time
-  static_assert(kIter % kN == 0, "a stage is a whole number of folds");
+  constexpr int kIter = kStageIter;
+  constexpr int kStageGran = kT * kIter;
+  constexpr int kStageBytes = stage_bytes(NW);
   extern __shared__ __align__(128) unsigned char ring[];
-  float4* part = reinterpret_cast<float4*>(ring + (size_t)q.stages * kStageBytes);
-  uint64_t* full = reinterpret_cast<uint64_t*>(part + 2 * kMaxCluster * NW);
+  const RingLayout lay = ring_layout(q.stages, NW);
+  float4* part = reinterpret_cast<float4*>(ring + lay.part);  // [2][C NW]
+  RowGrad* grad = reinterpret_cast<RowGrad*>(ring + lay.grad);  // [2], 32 bytes apart
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + lay.bars);
   uint64_t* empty = full + q.stages;
-  uint64_t* rowbar = empty + q.stages;  // [2]
-  int* abort_flag = reinterpret_cast<int*>(rowbar + 2);
+  uint64_t* sums_in = empty + q.stages;  // [2] a row's sums have arrived
+  uint64_t* result = sums_in + 2;        // [2] GRAD: its factors are there; else its sums are read
+  int* abort_flag = reinterpret_cast<int*>(ring + lay.flag);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = q.C;
@@ -519,8 +560,10 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 8 ? 2 : 6)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], NW);
     }
-    mbar_init(&rowbar[0], 1);
-    mbar_init(&rowbar[1], 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sums_in[s], 1);
+      mbar_init(&result[s], 1);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -540,7 +583,14 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 8 ? 2 : 6)
     atomicOr(p.status, kScoreTimeout);
     *(volatile int*)abort_flag = 1;
   };
+  // A barrier's phase has completed: one test and a vote, the bounded wait
+  // only where that fails.  The outcome is the whole warp's.
+  auto wait = [&](uint64_t* bar, uint32_t ph) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, ph))) return true;
+    return (bool)__all_sync(0xffffffffu, mbar_wait(bar, ph, p.wait_ns, abort_flag));
+  };
   bool ok = true;
+  const float nan = __int_as_float(0x7fc00000);
 
   if (warp == NW) {
     // ------------------------------------------------------------ producer
@@ -567,10 +617,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 8 ? 2 : 6)
       const int copies = GRAD && !q.resident ? 2 : 1;
       for (int c = 0; c < copies && ok; ++c) {
         for (int g = s.g0; g < s.g0 + s.n; g += kStageGran) {
-          // one lane waits, the warp goes on together
-          bool free = true;
-          if (lane == 0) free = mbar_wait(&empty[slot], phase, p.wait_ns, abort_flag);
-          if (!__all_sync(0xffffffffu, free)) {
+          if (!wait(&empty[slot], phase)) {
             ok = false;
             break;
           }
@@ -605,6 +652,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 8 ? 2 : 6)
               bulk_load(dst + (size_t)(b0 - g) * 16, img + (size_t)b0 * 16, bytes, &full[slot],
                         once);
           }
+          __syncwarp();
           ++issued;
           if (++slot == q.stages) {
             slot = 0;
@@ -619,13 +667,107 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 8 ? 2 : 6)
       for (int k = max(0, issued - q.stages); k < issued; ++k)
         mbar_wait(&full[k % q.stages], (uint32_t)(k / q.stages) & 1u, kDrainLimitNs);
     __syncwarp();
+  } else if (warp == NW + 1) {
+    // ------------------------------------------------------------ finisher
+    double t[kPolicyTerms] = {};
+    uint32_t count = 0;  // rows finished
+    const bool first = rank == 0;
+    if (GRAD || first) {
+      // a row's inputs, fetched one row ahead
+      int token = -1;
+      float weight = 1.f, T = p.temp, x0 = 0.f, x1 = 0.f, x2 = 0.f;
+      auto fetch = [&](int row) {
+        token = p.tokens[row];
+        if (p.weights) weight = p.weights[row];
+        if (p.temps) T = p.temps[row];
+        if (q.mode == kModePolicy) {
+          x0 = p.old_lp[row];
+          x1 = p.adv[row];
+          if (p.ref_lp) x2 = p.ref_lp[row];
+        } else if (q.mode == kModeGrad) {
+          x0 = p.g_lp[row];
+          if (p.g_h) x1 = p.g_h[row];
+        }
+      };
+      int i = cid;
+      if (i < p.rows) fetch(row_of(i));
+      for (; i < p.rows && ok; i += ncl) {
+        const int row = row_of(i);
+        const int a = token;
+        const float wt = weight, y0 = x0, y1 = x1, y2 = x2;
+        const float Trow = row_temp_ok(T) ? T : nan;
+        if (i + ncl < p.rows) fetch(row_of(i + ncl));
+        if (!live(row, a, wt)) {
+          if (first && lane == 0) {
+            if (p.logprobs) p.logprobs[row] = 0.f;
+            if (p.entropies) p.entropies[row] = 0.f;
+          }
+          continue;
+        }
+        const uint32_t par = count & 1u;
+        const float c2 = kLog2e / Trow;
+        if (lane == 0) mbar_arrive_expect_tx(&sums_in[par], (uint32_t)(C * NW * 16));
+        __syncwarp();
+        if (!wait(&sums_in[par], (count >> 1) & 1u)) {
+          ok = false;
+          break;
+        }
+        RowSums all = row_sums_empty();
+        float za = 0.f;  // the token's logit, from the warp that holds it
+        for (int k = lane; k < C * NW; k += 32) {
+          const float4 v = part[par * kMaxCluster * NW + k];
+          all = row_sums_join(all, RowSums{v.x, v.y, v.z}, c2);
+          za += v.w;
+        }
+        all = warp_join(all, c2);
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) za += __shfl_xor_sync(0xffffffffu, za, k);
+        if (!GRAD) {  // the slots are free again
+          __syncwarp();
+          if (lane < C) arrive_remote(map_rank(smem_u32(&result[par]), lane));
+        }
+        const bool bad = a >= p.V;
+        const RowResult r = row_result(all, bad ? nan : za, c2);
+        RowCoef c{y0, y1};
+        if (q.mode == kModePolicy)
+          c = policy_row(p, r, wt, y0, y1, y2, first && lane == 0, t);
+        if (GRAD) {
+          if (lane == 0) {
+            const float iT = 1.f / Trow;
+            RowGrad o;
+            o.M = r.M;
+            o.l2S = r.l2S;
+            o.a0 = -iT * (ENT ? fmaf(c.h, r.H, c.g) : c.g);
+            o.a1 = -iT * c.h * kLn2;
+            // p_a = 0: log p_a may be -inf, its entropy term is 0
+            const float ha = !ENT ? 0.f : r.pa > 0.f ? c.h * r.pa * (r.lp + r.H) : r.pa;
+            o.own = iT * (c.g * r.rest - ha);
+            *reinterpret_cast<RowGrad*>(reinterpret_cast<char*>(grad) + par * 32) = o;
+            mbar_arrive(&result[par]);
+          }
+          __syncwarp();
+        }
+        if (first && lane == 0) {
+          if (p.logprobs) p.logprobs[row] = r.lp;
+          if (ENT && p.entropies) p.entropies[row] = r.H;
+          const uint32_t bits = (bad ? kScoreBadToken : 0u) | (r.finite ? 0u : kScoreNonFinite);
+          if (bits) atomicOr(p.status, bits);
+        }
+        ++count;
+      }
+      if (!ok && lane == 0) fail();
+    }
+    if (q.mode == kModePolicy && first && lane == 0) {
+      const bool cut = !ok || *(volatile int*)abort_flag;
+      for (int k = 0; k < kPolicyTerms; ++k)
+        p.part[(size_t)cid * kPolicyTerms + k] = cut ? (double)nan : t[k];
+    }
+    __syncwarp();
   } else {
     // ----------------------------------------------------------- consumers
-    double t[kPolicyTerms] = {};
-    const bool writer = rank == 0 && warp == 0 && lane == 0;
     int slot = 0;
     uint32_t phase = 0;
-    uint32_t count = 0;  // rows exchanged
+    uint32_t count = 0;  // rows folded
     int i = cid;
     int token = -1;
     float weight = 1.f, T = p.temp;
@@ -638,7 +780,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 8 ? 2 : 6)
       const int row = row_of(i);
       const int a = token;
       const float wt = weight;
-      const float Trow = row_temp_ok(T) ? T : __int_as_float(0x7fc00000);
+      const float c2 = kLog2e / (row_temp_ok(T) ? T : nan);
       if (i + ncl < p.rows) {
         token = p.tokens[row_of(i + ncl)];
         if (p.weights) weight = p.weights[row_of(i + ncl)];
@@ -648,96 +790,70 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 8 ? 2 : 6)
       char* dz = nullptr;  // the gradient's image, aligned as the logits' (or element by element)
       bool dz_vec = false;
       if (GRAD) {
-        char* d = static_cast<char*>(p.d_logits) + (int64_t)row * p.ldd * kB;
-        dz = d - sh.shift * kB;
+        dz = static_cast<char*>(p.d_logits) + (int64_t)row * p.ldd * kB - sh.shift * kB;
         dz_vec = ((uintptr_t)dz & 15u) == 0;
       }
-      // the gradient's granule g: whole and aligned, or element by element
-      auto put = [&](int g, const uint4& w) {
-        if (dz_vec && g >= sh.whole0 && g < sh.whole1) {
-          *reinterpret_cast<uint4*>(dz + (int64_t)g * 16) = w;
-        } else {
-          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            const int v = g * kPer + k - sh.shift;
-            if (v < 0 || v >= p.V) continue;
-            if (kB == 4)
-              reinterpret_cast<uint32_t*>(dz)[(int64_t)g * kPer + k] = x[k & 3];
-            else
-              reinterpret_cast<uint16_t*>(dz)[(int64_t)g * kPer + k] =
-                  (uint16_t)(x[(k >> 1) & 3] >> (16 * (k & 1)));
-          }
-        }
-      };
       if (!live(row, a, wt)) {
-        if (writer) {
-          if (p.logprobs) p.logprobs[row] = 0.f;
-          if (p.entropies) p.entropies[row] = 0.f;
-        }
         if (GRAD)
-          for (int g = sh.g0 + tid; g < sh.g0 + sh.n; g += kT) put(g, make_uint4(0, 0, 0, 0));
+          for (int g = sh.g0 + tid; g < sh.g0 + sh.n; g += kT) {
+            if (dz_vec && g >= sh.whole0 && g < sh.whole1) {
+              *reinterpret_cast<uint4*>(dz + (int64_t)g * 16) = make_uint4(0, 0, 0, 0);
+            } else {
+#pragma unroll 1
+              for (int k = 0; k < kPer; ++k) {
+                const int v = g * kPer + k - sh.shift;
+                if (v >= 0 && v < p.V) store_grad<DT>(dz, (int64_t)g * kPer + k, 0.f);
+              }
+            }
+          }
         continue;
       }
-      const bool bad = a >= p.V;
-      const float za = bad ? __int_as_float(0x7fc00000)
-                           : load_logit<DT>(static_cast<const char*>(p.logits) +
-                                                (int64_t)row * p.ld * kB, a);
-      float x0 = 0.f, x1 = 0.f, x2 = 0.f;  // the mode's own inputs
-      if (q.mode == kModePolicy) {
-        x0 = p.old_lp[row];
-        x1 = p.adv[row];
-        if (p.ref_lp) x2 = p.ref_lp[row];
-      } else if (q.mode == kModeGrad) {
-        x0 = p.g_lp[row];
-        if (p.g_h) x1 = p.g_h[row];
-      }
-      const float c2 = kLog2e / Trow;
-      uint64_t* bar = &rowbar[count & 1u];
-      if (tid == 0) mbar_arrive_expect_tx(bar, (uint32_t)(C * NW * 16));
-
       // the token's place: this thread's granule `mine` (counted along its own
       // granules), element `el`
       int mine = -1;
       const int at = a + sh.shift, ag = at / kPer - sh.g0, el = at & (kPer - 1);
-      if (!bad && ag >= 0 && ag < sh.n && (ag & (kT - 1)) == tid) mine = ag / kT;
+      const bool here = a < p.V && ag >= 0 && ag < sh.n;
+      if (here && (ag & (kT - 1)) == tid) mine = ag / kT;
 
       // pass 1: the sums
       ThreadSums s;
       s.m = -FLT_MAX;
       s.R[0] = s.R[1] = s.Q[0] = s.Q[1] = 0ull;
       bool deep = false;
+      float za = 0.f;
       const int slot0 = slot;
-      int n = sh.n;  // granules left
-      int it = 0;
+      int n = sh.n;   // granules left
+      int first = 0;  // the stage's first granule of this thread
       while (n > 0) {
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait(&full[slot], phase, p.wait_ns, abort_flag))) {
+        if (!wait(&full[slot], phase)) {
           ok = false;
           break;
         }
-        const uint4* st = reinterpret_cast<const uint4*>(ring + (size_t)slot * kStageBytes);
+        const uint4* st = reinterpret_cast<const uint4*>(ring + (size_t)slot * kStageBytes) + tid;
+        const int drop =
+            (unsigned)(mine - first) < (unsigned)kIter ? (mine - first) * kPer + el : -1;
+        if (n >= kStageGran) {
+          uint4 w[kIter];
 #pragma unroll
-        for (int j = 0; j < kIter; j += kN) {
-          if (j * kT + tid >= n) break;
-          uint4 w[kN];
-#pragma unroll
-          for (int k = 0; k < kN; ++k) {
-            const int g = (j + k) * kT + tid;
-            if (g < n)
-              w[k] = st[g];
-            else  // past the share: nothing
-              w[k] = kB == 4 ? make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u)
-                             : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-            if (it + j + k == mine) granule_drop<DT>(w[k], el);
+          for (int j = 0; j < kIter; ++j) w[j] = st[j * kT];
+          fold<DT, ENT, kIter>(s, w, st, kT, drop, c2, sh.g0 + first * kT + tid, sh.whole0,
+                               sh.whole1, za, deep);
+        } else {
+          // the share's last granules, one at a time
+#pragma unroll 1
+          for (int j = 0; j < kIter && j * kT + tid < n; ++j) {
+            const uint4 w[1] = {st[j * kT]};
+            const int dj = drop >= j * kPer && drop < (j + 1) * kPer ? drop - j * kPer : -1;
+            fold<DT, ENT, 1>(s, w, st + j * kT, kT, dj, c2, sh.g0 + (first + j) * kT + tid,
+                             sh.whole0, sh.whole1, za, deep);
           }
-          fold<DT, ENT, kN>(s, w, c2, deep);
+          __syncwarp();
         }
         if (!GRAD || !q.resident) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&empty[slot]);
         }
-        it += kIter;
+        first += kIter;
         n -= kStageGran;
         if (++slot == q.stages) {
           slot = 0;
@@ -745,95 +861,97 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 8 ? 2 : 6)
         }
       }
       if (!ok) break;
-      // this warp's sums to every CTA of the cluster (the token's logit rides
-      // along: it has been read before any CTA may overwrite the row)
-      RowSums rs = warp_join(RowSums{s.m, pair_sum(s.R), ENT ? pair_sum(s.Q) : 0.f}, c2);
-      if (lane < C) {
-        const uint32_t to = smem_u32(&part[(count & 1u) * kMaxCluster * NW + rank * NW + warp]);
-        st_async4(map_rank(to, lane), rs.m, rs.R, rs.Q, za, map_rank(smem_u32(bar), lane));
-      }
-      if (!__all_sync(0xffffffffu, mbar_wait(bar, (count >> 1) & 1u, p.wait_ns, abort_flag))) {
+      // this warp's sums to the finishing CTAs, with the token's logit where
+      // this warp holds it
+      const uint32_t par = count & 1u;
+      const RowSums rs = warp_join(RowSums{s.m, pair_sum(s.R), ENT ? pair_sum(s.Q) : 0.f}, c2);
+      const int holder = here ? ag & (kT - 1) : -1;
+      za = __shfl_sync(0xffffffffu, za, holder & 31);
+      if (!here || (holder >> 5) != warp) za = 0.f;
+      // without a gradient nothing else holds this warp back: the slots must
+      // have been read two rows ago
+      if (!GRAD && count >= 2 && !wait(&result[par], ((count >> 1) - 1u) & 1u)) {
         ok = false;
         break;
       }
-      RowSums all = row_sums_empty();
-      for (int k = lane; k < C * NW; k += 32) {
-        const float4 v = part[(count & 1u) * kMaxCluster * NW + k];
-        all = row_sums_join(all, RowSums{v.x, v.y, v.z}, c2);
+      if (lane < (GRAD ? C : 1)) {
+        const uint32_t to = smem_u32(&part[par * kMaxCluster * NW + rank * NW + warp]);
+        st_async4(map_rank(to, lane), rs.m, rs.R, rs.Q, za,
+                  map_rank(smem_u32(&sums_in[par]), lane));
       }
-      all = warp_join(all, c2);
       ++count;
-      const RowResult r = row_result(all, za, c2);
-      RowCoef c{0.f, 0.f};
-      if (q.mode == kModePolicy) {
-        c = policy_row(p, r, wt, x0, x1, x2, writer, t);
-      } else {
-        c.g = x0;
-        c.h = x1;
-      }
-      if (writer) {
-        if (p.logprobs) p.logprobs[row] = r.lp;
-        if (ENT && p.entropies) p.entropies[row] = r.H;
-        const uint32_t bits = (bad ? kScoreBadToken : 0u) | (r.finite ? 0u : kScoreNonFinite);
-        if (bits) atomicOr(p.status, bits);
-      }
       if (!GRAD) continue;
 
       // pass 2: the gradient, from the stages that still hold the row
-      const float iT = 1.f / Trow;
-      const float a0 = -iT * (ENT ? fmaf(c.h, r.H, c.g) : c.g), a1 = -iT * c.h * kLn2;
-      // p_a = 0: log p_a may be -inf, its entropy term is 0
-      const float ha = !ENT ? 0.f : r.pa > 0.f ? c.h * r.pa * (r.lp + r.H) : r.pa;
-      const float own = iT * (c.g * r.rest - ha);
+      if (!wait(&result[par], ((count - 1u) >> 1) & 1u)) {
+        ok = false;
+        break;
+      }
+      const RowGrad r = *reinterpret_cast<const RowGrad*>(reinterpret_cast<char*>(grad) + par * 32);
       const uint64_t nM = pack2(-r.M, -r.M), cc = pack2(c2, c2), nl = pack2(-r.l2S, -r.l2S),
-                     A0 = pack2(a0, a0), A1 = pack2(a1, a1);
+                     A0 = pack2(r.a0, r.a0), A1 = pack2(r.a1, r.a1);
       if (ENT && (s.m - r.M) * c2 < -kDeep) deep = true;
       if (q.resident) slot = slot0;
       n = sh.n;
-      it = 0;
+      first = 0;
       int g = sh.g0 + tid;
       while (n > 0) {
-        if (!q.resident &&
-            !__all_sync(0xffffffffu, mbar_wait(&full[slot], phase, p.wait_ns, abort_flag))) {
+        if (!q.resident && !wait(&full[slot], phase)) {
           ok = false;
           break;
         }
-        const uint4* st = reinterpret_cast<const uint4*>(ring + (size_t)slot * kStageBytes);
-#pragma unroll
-        for (int j = 0; j < kIter; ++j, g += kT) {
-          if (j * kT + tid >= n) continue;
-          const Granule<DT> z = granule<DT>(st[j * kT + tid]);
+        const uint4* st = reinterpret_cast<const uint4*>(ring + (size_t)slot * kStageBytes) + tid;
+        auto granule_grad = [&](const uint4& raw) {
+          const Granule<DT> z = granule<DT>(raw);
           float o[kPer];
 #pragma unroll
           for (int k = 0; k < kPer / 2; ++k) {
-            uint64_t x = fma2(add2(z.v[k], nM), cc, nl);
+            const uint64_t x = fma2(add2(z.v[k], nM), cc, nl);
             float xa, xb;
             unpack2(x, xa, xb);
-            if (ENT && deep) {
-              xa = xa < -kDeep ? -kDeep : xa;
-              xb = xb < -kDeep ? -kDeep : xb;
-              x = pack2(xa, xb);
-            }
             const uint64_t e = pack2(ex2(xa), ex2(xb));
             unpack2(mul2(e, ENT ? fma2(A1, x, A0) : A0), o[2 * k], o[2 * k + 1]);
           }
-          if (it + j == mine) {
-#pragma unroll
-            for (int k = 0; k < kPer; ++k)
-              if (k == el) o[k] = own;
-          }
-          uint4 w;
           if constexpr (DT == kScoreF32)
-            w = make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]),
-                           __float_as_uint(o[3]));
+            return make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]),
+                              __float_as_uint(o[3]));
           else
-            w = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
-                           pack_bf16(o[6], o[7]));
-          put(g, w);
+            return make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
+                              pack_bf16(o[6], o[7]));
+        };
+        // a stage of whole granules without the token, nothing to clamp
+        const bool plain = n >= kStageGran && dz_vec && !deep &&
+                           (unsigned)(mine - first) >= (unsigned)kIter && g >= sh.whole0 &&
+                           g + (kIter - 1) * kT < sh.whole1;
+        if (plain) {
+          uint4* out = reinterpret_cast<uint4*>(dz) + g;
+#pragma unroll
+          for (int j = 0; j < kIter; ++j) out[j * kT] = granule_grad(st[j * kT]);
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < kIter && j * kT + tid < n; ++j) {
+            const int gj = g + j * kT;
+            if (!deep && first + j != mine && dz_vec && gj >= sh.whole0 && gj < sh.whole1) {
+              reinterpret_cast<uint4*>(dz)[gj] = granule_grad(st[j * kT]);
+              continue;
+            }
+#pragma unroll 1
+            for (int k = 0; k < kPer; ++k) {
+              const int v = gj * kPer + k - sh.shift;
+              if (v < 0 || v >= p.V) continue;
+              float x = (load_logit<DT>(st + j * kT, k) - r.M) * c2;
+              if (ENT) x = x < -kDeep ? -kDeep : x;
+              x -= r.l2S;
+              const float o = ex2(x) * (ENT ? fmaf(r.a1, x, r.a0) : r.a0);
+              store_grad<DT>(dz, (int64_t)gj * kPer + k,
+                             first + j == mine && k == el ? r.own : o);
+            }
+          }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[slot]);
-        it += kIter;
+        first += kIter;
+        g += kIter * kT;
         n -= kStageGran;
         if (++slot == q.stages) {
           slot = 0;
@@ -848,13 +966,10 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 8 ? 2 : 6)
       __nanosleep(100000);
       __syncwarp();
     }
-    if (q.mode == kModePolicy && writer)
-      for (int k = 0; k < kPolicyTerms; ++k)
-        p.part[(size_t)cid * kPolicyTerms + k] = ok ? t[k] : (double)__int_as_float(0x7fc00000);
   }
   __syncthreads();
   cluster_sync_all();
-  if (q.mode == kModePolicy && rank == 0) policy_total<NW>(p, ncl);
+  if (q.mode == kModePolicy && rank == 0) policy_total<NW + 2>(p, ncl);
 }
 
 // ---------------------------------------------------------------------------
