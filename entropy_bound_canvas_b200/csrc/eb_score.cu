@@ -54,7 +54,7 @@ size_t ring_smem_of(bool wide) {
 }
 constexpr int64_t kNarrowBytes = 16384;  // rows up to this take the narrow form
 constexpr int kShareStages = 4;          // a wide CTA's share where the cluster allows it
-constexpr int kMaxC = 8;
+constexpr int kMaxLog2C = 3;
 
 struct DeviceInfo {
   std::once_flag once;
@@ -167,8 +167,9 @@ void fill_args(const eb_scorer* h, const eb_score_input_t* in, ScoreArgs& a) {
 // How a launch over rows is laid out.
 struct RingPlan {
   int wide;      // 8 consumer warps and a large ring, else 4 and a small one
-  int C;         // CTAs per row
-  int resident;  // a CTA's share of a row fits its ring
+  int log2C;     // CTAs per row
+  int resident;  // a row's stages are kept until its gradient
+  int ahead;     // the next row is folded before this one's gradient
 };
 
 int share_stages(int64_t row_bytes, int C, int warps) {
@@ -182,13 +183,18 @@ int share_stages(int64_t row_bytes, int C, int warps) {
 RingPlan ring_plan(int sms, int64_t rows, int64_t row_bytes) {
   RingPlan r;
   r.wide = row_bytes > kNarrowBytes;
-  r.C = 1;
+  r.log2C = 0;
+  const int warps = r.wide ? 8 : 4, stages = r.wide ? kWideStages : kNarrowStages;
   if (r.wide) {
-    while (r.C < kMaxC && share_stages(row_bytes, r.C, 8) > kShareStages) r.C *= 2;
-    while (r.C < kMaxC && rows * r.C * 2 <= 2 * sms && row_bytes / r.C > ebk::stage_bytes(8))
-      r.C *= 2;
+    while (r.log2C < kMaxLog2C && share_stages(row_bytes, 1 << r.log2C, 8) > kShareStages)
+      ++r.log2C;
+    while (r.log2C < kMaxLog2C && (rows << (r.log2C + 1)) <= 2 * sms &&
+           (row_bytes >> r.log2C) > ebk::stage_bytes(8))
+      ++r.log2C;
   }
-  r.resident = share_stages(row_bytes, r.C, r.wide ? 8 : 4) <= (r.wide ? kWideStages : kNarrowStages);
+  const int share = share_stages(row_bytes, 1 << r.log2C, warps);
+  r.resident = 2 * share <= stages;
+  r.ahead = 1;
   return r;
 }
 
@@ -200,9 +206,10 @@ int launch_rows(const eb_scorer* h, const ScoreArgs& a, int dtype, int mode, boo
   ebk::RingArgs q;
   q.mode = mode;
   q.reverse = reverse ? 1 : 0;
-  q.C = r.C;
+  q.log2C = r.log2C;
   q.stages = r.wide ? kWideStages : kNarrowStages;
   q.resident = r.resident;
+  q.ahead = r.ahead;
   cudaLaunchConfig_t lc;
   std::memset(&lc, 0, sizeof(lc));
   lc.blockDim = dim3((warps + 2) * 32);
@@ -210,15 +217,15 @@ int launch_rows(const eb_scorer* h, const ScoreArgs& a, int dtype, int mode, boo
   lc.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = r.C;
+  attr[0].val.clusterDim.x = 1 << r.log2C;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
   // the clusters that fit the device at once, asked once per variant and size
-  std::atomic<int>& cached = g_info[h->device].clusters[v][__builtin_ctz(r.C)];
+  std::atomic<int>& cached = g_info[h->device].clusters[v][r.log2C];
   int most = cached.load(std::memory_order_relaxed);
   if (most == 0) {
-    lc.gridDim = dim3(r.C);
+    lc.gridDim = dim3(1 << r.log2C);
     if (cudaOccupancyMaxActiveClusters(&most, kRing[v], &lc) != cudaSuccess || most < 1) {
       cudaGetLastError();
       return EB_ERR_CUDA;
@@ -226,7 +233,7 @@ int launch_rows(const eb_scorer* h, const ScoreArgs& a, int dtype, int mode, boo
     most = std::min(most, kMaxGrid);
     cached.store(most, std::memory_order_relaxed);
   }
-  lc.gridDim = dim3(std::max(1, std::min(a.rows, most)) * r.C);
+  lc.gridDim = dim3(std::max(1, std::min(a.rows, most)) << r.log2C);
   void* args[] = {const_cast<ScoreArgs*>(&a), &q};
   return cudaLaunchKernelExC(&lc, kRing[v], args) == cudaSuccess ? EB_OK : EB_ERR_CUDA;
 }

@@ -246,10 +246,11 @@ __device__ __forceinline__ void policy_total(const ScoreArgs& p, int n) {
 //              computes the row's results and its gradient's factors.
 // Without a gradient only the first CTA finishes, and the consumers go on to
 // the next row at once.  With one every CTA does (the same arithmetic, the
-// same bits): the stages are kept until its finisher has the factors, and the
-// same threads turn what they hold into the gradient, so the logits are read
-// from HBM once.  Freed stages take the next row's copy at once.  A share
-// longer than the ring (resident = 0) is copied a second time instead.
+// same bits), and the consumers fold the next row before they turn this one
+// into its gradient, so that the exchange and the finisher's work run under
+// that.  Where two shares fit the ring (resident) a row's stages are kept
+// until then.  Otherwise its share is copied a second time, from L2: a row
+// per cluster, two in flight, stay there (the first copy asks for it).
 //
 // Rows start at any element.  A share is a range of 16-byte granules of the
 // row's 16-byte-aligned image; the granules that the row fills only partly
@@ -267,10 +268,12 @@ constexpr float kLazy = 2.0f;
 
 struct RingArgs {
   int mode, reverse;
-  int C;         // CTAs per cluster
+  int log2C;     // CTAs per cluster: a power of two
   int stages;    // of the ring
-  int resident;  // a share fits the ring: copied once
+  int resident;  // rows are kept in the ring until their gradient: copied once
+  int ahead;     // the next row is folded before this one's gradient (resident: two shares fit)
 };
+constexpr int kSlots = 4;  // rows between a slot's uses, see the kernel
 
 // What the consumers need for a row's gradient.
 struct RowGrad {
@@ -285,9 +288,9 @@ struct RingLayout {
 __host__ __device__ constexpr RingLayout ring_layout(int stages, int warps) {
   RingLayout y{};
   y.part = (uint32_t)(stages * stage_bytes(warps));
-  y.grad = y.part + 2u * kMaxCluster * (uint32_t)warps * 16u;
-  y.bars = y.grad + 2u * 32u;
-  y.flag = y.bars + (2u * (uint32_t)stages + 6u) * 8u;
+  y.grad = y.part + (uint32_t)(kSlots * kMaxCluster * warps * 16);
+  y.bars = y.grad + kSlots * 32u;
+  y.flag = y.bars + (2u * (uint32_t)stages + 2u * kSlots) * 8u;
   y.total = y.flag + 16u;
   return y;
 }
@@ -353,6 +356,11 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Written once, not read again here: first to leave L2.
+__device__ __forceinline__ void store_stream(uint4* p, const uint4& v) {
+  __stcs(p, v);
+}
+
 // One granule of 16 bytes as packed fp32 pairs.
 template <int DT>
 struct Granule {
@@ -396,6 +404,33 @@ __device__ __forceinline__ float granule_max(const uint4 (&w)[N]) {
   }
 }
 
+// Element `at` of N granules, replaced by -inf.
+template <int DT, int N>
+__device__ __forceinline__ float granule_drop(uint4 (&w)[N], int at) {
+  constexpr int kPer = ScoreType<DT>::kPer16, kWord = kPer / 4;  // elements per 32-bit word
+  float z = 0.f;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    uint32_t x[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (n * 4 + k != at / kWord) continue;
+      if (DT == kScoreF32) {
+        z = __uint_as_float(x[k]);
+        x[k] = 0xff800000u;
+      } else if (at & 1) {
+        z = bf_hi(x[k]);
+        x[k] = (x[k] & 0xffffu) | 0xff800000u;
+      } else {
+        z = bf_lo(x[k]);
+        x[k] = (x[k] & 0xffff0000u) | 0xff80u;
+      }
+    }
+    w[n] = make_uint4(x[0], x[1], x[2], x[3]);
+  }
+  return z;
+}
+
 // A thread's running sums: pairs, two chains each.
 struct ThreadSums {
   float m;
@@ -408,15 +443,41 @@ __device__ __forceinline__ float pair_sum(const uint64_t (&v)[2]) {
   return a + b;
 }
 
-// Folds N granules, held in w and at st[k step] in shared memory.  `drop`: the
-// element that is left out (counted through the N granules), or -1; its value
-// goes to `za`.  `deep` is set by elements of whole granules (numbers whole0 ..
-// whole1 - 1, the first one here being g) so far below the reference that
-// their exponent has to be clamped.
+// Sums of N granules against the reference m.  CLAMP: exponents are held at
+// -kDeep (e = 0 there), and `low` gets a bit for each granule that needed it.
+template <int DT, bool ENT, bool CLAMP, int N>
+__device__ __forceinline__ void granule_sums(const uint4 (&w)[N], float m, float c2,
+                                             uint64_t (&R)[2], uint64_t (&Q)[2], unsigned& low) {
+  const uint64_t nm = pack2(-m, -m), cc = pack2(c2, c2);
+  R[0] = R[1] = Q[0] = Q[1] = 0ull;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const Granule<DT> v = granule<DT>(w[n]);
+#pragma unroll
+    for (int k = 0; k < Granule<DT>::kPairs; ++k) {
+      uint64_t d = mul2(add2(v.v[k], nm), cc);
+      float d0, d1;
+      unpack2(d, d0, d1);
+      if (CLAMP) {  // by comparison, so that NaN stays NaN
+        if (d0 < -kDeep || d1 < -kDeep) low |= 1u << n;
+        d0 = d0 < -kDeep ? -kDeep : d0;
+        d1 = d1 < -kDeep ? -kDeep : d1;
+        d = pack2(d0, d1);
+      }
+      const uint64_t e = pack2(ex2(d0), ex2(d1));
+      R[k & 1] = add2(R[k & 1], e);
+      if (ENT) Q[k & 1] = fma2(e, d, Q[k & 1]);
+    }
+  }
+}
+
+// Folds N granules into a thread's sums.  `drop`: the element that is left out
+// (counted through the N granules), or -1; its value goes to `za`.  `low`: the
+// granules with elements so far below the reference that their exponent has
+// to be clamped.
 template <int DT, bool ENT, int N>
-__device__ __forceinline__ void fold(ThreadSums& s, const uint4 (&w)[N], const uint4* st, int step,
-                                     int drop, float c2, int g, int whole0, int whole1, float& za,
-                                     bool& deep) {
+__device__ __forceinline__ void fold(ThreadSums& s, uint4 (&w)[N], int drop, float c2, float& za,
+                                     unsigned& low) {
   const float hi = granule_max<DT, N>(w);
   if ((hi - s.m) * c2 > kLazy) {  // also from the empty reference -FLT_MAX
     const float d = fmaxf((s.m - hi) * c2, -kDeep), f = ex2(d);
@@ -428,57 +489,53 @@ __device__ __forceinline__ void fold(ThreadSums& s, const uint4 (&w)[N], const u
     }
     s.m = hi;
   }
-  const uint64_t nm = pack2(-s.m, -s.m), cc = pack2(c2, c2);
-  uint64_t R[2] = {0ull, 0ull}, Q[2] = {0ull, 0ull};
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const Granule<DT> v = granule<DT>(w[n]);
-#pragma unroll
-    for (int k = 0; k < Granule<DT>::kPairs; ++k) {
-      const uint64_t d = mul2(add2(v.v[k], nm), cc);
-      float d0, d1;
-      unpack2(d, d0, d1);
-      const uint64_t e = pack2(ex2(d0), ex2(d1));
-      R[k & 1] = add2(R[k & 1], e);
-      if (ENT) Q[k & 1] = fma2(e, d, Q[k & 1]);
-    }
-  }
+  uint64_t R[2], Q[2];
+  granule_sums<DT, ENT, false, N>(w, s.m, c2, R, Q, low);
   bool again = drop >= 0;
-  if (ENT) {
-    // an exponent of -inf makes e d NaN
+  if (ENT) {  // an exponent of -inf makes e d NaN
     const float t = pair_sum(Q);
     again = again || t != t;
   }
   if (again) {
-    // rare: element by element, with the clamp and without the dropped one
-    constexpr int kPer = ScoreType<DT>::kPer16;
-    float r1 = 0.f, q1 = 0.f;
-#pragma unroll 1
-    for (int e = 0; e < N * kPer; ++e) {
-      const int off = (e / kPer) * step;
-      const float z = load_logit<DT>(st + off, e % kPer);
-      if (e == drop) {
-        za = z;
-        continue;
-      }
-      float d = (z - s.m) * c2;
-      if (d < -kDeep) {
-        d = -kDeep;
-        if (g + off >= whole0 && g + off < whole1) deep = true;
-      }
-      const float x = ex2(d);
-      r1 += x;
-      q1 = fmaf(x, d, q1);
-    }
-    R[0] = pack2(r1, 0.f);
-    Q[0] = pack2(q1, 0.f);
-    R[1] = Q[1] = 0ull;
+    if (drop >= 0) za = granule_drop<DT, N>(w, drop);
+    granule_sums<DT, ENT, true, N>(w, s.m, c2, R, Q, low);
   }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     s.R[k] = add2(s.R[k], R[k]);
     if (ENT) s.Q[k] = add2(s.Q[k], Q[k]);
   }
+}
+
+// The gradient p (a0 + a1 log2 p), p = 2^((z - M) c2 - l2S), of a granule.
+template <int DT, bool ENT, bool CLAMP>
+__device__ __forceinline__ void granule_grad(const uint4& w, uint64_t nM, uint64_t c2, uint64_t nl,
+                                             uint64_t A0, uint64_t A1,
+                                             float (&o)[ScoreType<DT>::kPer16]) {
+  const Granule<DT> z = granule<DT>(w);
+#pragma unroll
+  for (int k = 0; k < Granule<DT>::kPairs; ++k) {
+    uint64_t x = fma2(add2(z.v[k], nM), c2, nl);
+    float xa, xb;
+    unpack2(x, xa, xb);
+    if (ENT && CLAMP) {
+      xa = xa < -kDeep ? -kDeep : xa;
+      xb = xb < -kDeep ? -kDeep : xb;
+      x = pack2(xa, xb);
+    }
+    const uint64_t e = pack2(ex2(xa), ex2(xb));
+    unpack2(mul2(e, ENT ? fma2(A1, x, A0) : A0), o[2 * k], o[2 * k + 1]);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ uint4 granule_pack(const float (&o)[ScoreType<DT>::kPer16]) {
+  if constexpr (DT == kScoreF32)
+    return make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]),
+                      __float_as_uint(o[3]));
+  else
+    return make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
+                      pack_bf16(o[6], o[7]));
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -509,8 +566,8 @@ struct RowShare {
 };
 
 template <int DT>
-__device__ __forceinline__ RowShare row_share(const void* buf, int64_t ld, int row, int V, int C,
-                                              int rank) {
+__device__ __forceinline__ RowShare row_share(const void* buf, int64_t ld, int row, int V,
+                                              int log2C, int rank) {
   constexpr int kB = ScoreType<DT>::kBytes, kPer = ScoreType<DT>::kPer16;
   RowShare s;
   const int64_t off = (int64_t)row * ld * kB;
@@ -519,7 +576,7 @@ __device__ __forceinline__ RowShare row_share(const void* buf, int64_t ld, int r
   s.shift = mis / kB;
   const int end = s.shift + V;
   const int G = (end + kPer - 1) / kPer;
-  const int per = ((G + C - 1) / C + 7) & ~7;
+  const int per = (((G + (1 << log2C) - 1) >> log2C) + 7) & ~7;
   s.g0 = min(G, rank * per);
   s.n = min(G - s.g0, per);
   s.whole0 = s.shift ? 1 : 0;
@@ -543,24 +600,24 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
   constexpr int kStageBytes = stage_bytes(NW);
   extern __shared__ __align__(128) unsigned char ring[];
   const RingLayout lay = ring_layout(q.stages, NW);
-  float4* part = reinterpret_cast<float4*>(ring + lay.part);  // [2][C NW]
-  RowGrad* grad = reinterpret_cast<RowGrad*>(ring + lay.grad);  // [2], 32 bytes apart
+  float4* part = reinterpret_cast<float4*>(ring + lay.part);  // [kSlots][C NW]
+  RowGrad* grad = reinterpret_cast<RowGrad*>(ring + lay.grad);  // [kSlots], 32 bytes apart
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + lay.bars);
   uint64_t* empty = full + q.stages;
-  uint64_t* sums_in = empty + q.stages;  // [2] a row's sums have arrived
-  uint64_t* result = sums_in + 2;        // [2] GRAD: its factors are there; else its sums are read
+  uint64_t* sums_in = empty + q.stages;  // [kSlots] a row's sums have arrived
+  uint64_t* result = sums_in + kSlots;   // [kSlots] its factors are there (no gradient: its sums are read)
   int* abort_flag = reinterpret_cast<int*>(ring + lay.flag);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int C = q.C;
+  const int C = 1 << q.log2C;
   const int rank = (int)cluster_rank();
-  const int cid = blockIdx.x / C, ncl = gridDim.x / C;
+  const int cid = blockIdx.x >> q.log2C, ncl = gridDim.x >> q.log2C;
   if (tid == 0) {
     for (int s = 0; s < q.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], NW);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kSlots; ++s) {
       mbar_init(&sums_in[s], 1);
       mbar_init(&result[s], 1);
     }
@@ -594,11 +651,58 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
 
   if (warp == NW) {
     // ------------------------------------------------------------ producer
-    const uint64_t once = evict_first_policy();
+    const uint64_t once = evict_first_policy(), again = evict_last_policy();
     int issued = 0, slot = 0;
     uint32_t phase = 1;  // the parity of an empty stage's first wait: passes at once
+    auto copy_share = [&](int row, uint64_t policy) {
+      const RowShare s = row_share<DT>(p.logits, p.ld, row, p.V, q.log2C, rank);
+      const char* img = static_cast<const char*>(p.logits) + s.base;
+      for (int g = s.g0; g < s.g0 + s.n; g += kStageGran) {
+        if (!wait(&empty[slot], phase)) {
+          ok = false;
+          break;
+        }
+        unsigned char* dst = ring + (size_t)slot * kStageBytes;
+        const int end = min(g + kStageGran, s.g0 + s.n);
+        const int b0 = max(g, s.whole0), b1 = max(b0, min(end, s.whole1));
+        if (b0 != g || b1 != end) {
+          // granules the row fills in part: at most the first and the last
+          for (int e = lane; e < 2 * kPer; e += 32) {
+            const int gr = e < kPer ? 0 : s.whole1;
+            const bool mine = gr >= g && gr < end && (gr < b0 || gr >= b1) &&
+                              (e < kPer || s.whole1 != 0 || s.whole0 == 0);
+            const int at = gr * kPer + (e & (kPer - 1));  // element of the image
+            if (mine) {
+              const int v = at - s.shift;
+              const bool in = v >= 0 && v < p.V;
+              unsigned char* to = dst + (size_t)(gr - g) * 16 + (e & (kPer - 1)) * kB;
+              if (kB == 4)
+                *reinterpret_cast<uint32_t*>(to) =
+                    in ? reinterpret_cast<const uint32_t*>(img)[at] : 0xff800000u;
+              else
+                *reinterpret_cast<uint16_t*>(to) =
+                    in ? reinterpret_cast<const uint16_t*>(img)[at] : (uint16_t)0xff80u;
+            }
+          }
+          __syncwarp();
+        }
+        if (lane == 0) {
+          const uint32_t bytes = (uint32_t)(b1 - b0) * 16u;
+          mbar_arrive_expect_tx(&full[slot], bytes);
+          if (bytes)
+            bulk_load(dst + (size_t)(b0 - g) * 16, img + (size_t)b0 * 16, bytes, &full[slot],
+                      policy);
+        }
+        __syncwarp();
+        ++issued;
+        if (++slot == q.stages) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+    };
     int i = cid;
-    int token = -1;
+    int token = -1, before = -1;  // before: a row still to be copied again
     float weight = 1.f;
     if (i < p.rows) {
       token = p.tokens[row_of(i)];
@@ -612,55 +716,15 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
         if (p.weights) weight = p.weights[row_of(i + ncl)];
       }
       if (!on) continue;
-      const RowShare s = row_share<DT>(p.logits, p.ld, row, p.V, C, rank);
-      const char* img = static_cast<const char*>(p.logits) + s.base;
-      const int copies = GRAD && !q.resident ? 2 : 1;
-      for (int c = 0; c < copies && ok; ++c) {
-        for (int g = s.g0; g < s.g0 + s.n; g += kStageGran) {
-          if (!wait(&empty[slot], phase)) {
-            ok = false;
-            break;
-          }
-          unsigned char* dst = ring + (size_t)slot * kStageBytes;
-          const int end = min(g + kStageGran, s.g0 + s.n);
-          const int b0 = max(g, s.whole0), b1 = max(b0, min(end, s.whole1));
-          if (b0 != g || b1 != end) {
-            // granules the row fills in part: at most the first and the last
-            for (int e = lane; e < 2 * kPer; e += 32) {
-              const int gr = e < kPer ? 0 : s.whole1;
-              const bool mine = gr >= g && gr < end && (gr < b0 || gr >= b1) &&
-                                (e < kPer || s.whole1 != 0 || s.whole0 == 0);
-              const int at = gr * kPer + (e & (kPer - 1));  // element of the image
-              if (mine) {
-                const int v = at - s.shift;
-                const bool in = v >= 0 && v < p.V;
-                unsigned char* to = dst + (size_t)(gr - g) * 16 + (e & (kPer - 1)) * kB;
-                if (kB == 4)
-                  *reinterpret_cast<uint32_t*>(to) =
-                      in ? reinterpret_cast<const uint32_t*>(img)[at] : 0xff800000u;
-                else
-                  *reinterpret_cast<uint16_t*>(to) =
-                      in ? reinterpret_cast<const uint16_t*>(img)[at] : (uint16_t)0xff80u;
-              }
-            }
-            __syncwarp();
-          }
-          if (lane == 0) {
-            const uint32_t bytes = (uint32_t)(b1 - b0) * 16u;
-            mbar_arrive_expect_tx(&full[slot], bytes);
-            if (bytes)
-              bulk_load(dst + (size_t)(b0 - g) * 16, img + (size_t)b0 * 16, bytes, &full[slot],
-                        once);
-          }
-          __syncwarp();
-          ++issued;
-          if (++slot == q.stages) {
-            slot = 0;
-            phase ^= 1u;
-          }
-        }
+      const bool twice = GRAD && !q.resident;
+      copy_share(row, twice ? again : once);
+      if (twice) {
+        if (!q.ahead) before = row;
+        if (before >= 0 && ok) copy_share(before, once);
+        before = q.ahead ? row : -1;
       }
     }
+    if (before >= 0 && ok) copy_share(before, once);
     if (!ok && lane == 0) fail();
     // every copy issued has landed before the CTA may leave
     if (lane == 0)
@@ -704,24 +768,41 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
           }
           continue;
         }
-        const uint32_t par = count & 1u;
+        const uint32_t par = count % kSlots, ph = (count / kSlots) & 1u;
         const float c2 = kLog2e / Trow;
         if (lane == 0) mbar_arrive_expect_tx(&sums_in[par], (uint32_t)(C * NW * 16));
         __syncwarp();
-        if (!wait(&sums_in[par], (count >> 1) & 1u)) {
+        if (!wait(&sums_in[par], ph)) {
           ok = false;
           break;
         }
-        RowSums all = row_sums_empty();
-        float za = 0.f;  // the token's logit, from the warp that holds it
-        for (int k = lane; k < C * NW; k += 32) {
-          const float4 v = part[par * kMaxCluster * NW + k];
-          all = row_sums_join(all, RowSums{v.x, v.y, v.z}, c2);
-          za += v.w;
-        }
-        all = warp_join(all, c2);
+        // the warps' sums against their largest reference; the token's logit
+        // comes from the warp that holds it, the others send 0
+        float4 v[kMaxCluster * NW / 32];
+        float m = -FLT_MAX;
 #pragma unroll
-        for (int k = 16; k > 0; k >>= 1) za += __shfl_xor_sync(0xffffffffu, za, k);
+        for (int k = 0; k < kMaxCluster * NW / 32; ++k) {
+          const int e = lane + 32 * k;
+          v[k] = e < C * NW ? part[par * kMaxCluster * NW + e]
+                            : make_float4(-FLT_MAX, 0.f, 0.f, 0.f);
+          m = fmaxf(m, v[k].x);
+        }
+        m = warp_max(m);
+        RowSums all{m, 0.f, 0.f};
+        float za = 0.f;
+#pragma unroll
+        for (int k = 0; k < kMaxCluster * NW / 32; ++k) {
+          const float d = fmaxf((v[k].x - m) * c2, -kDeep), f = ex2(d);
+          all.R = fmaf(f, v[k].y, all.R);
+          all.Q = fmaf(f, fmaf(d, v[k].y, v[k].z), all.Q);
+          za += v[k].w;
+        }
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) {
+          all.R += __shfl_xor_sync(0xffffffffu, all.R, k);
+          all.Q += __shfl_xor_sync(0xffffffffu, all.Q, k);
+          za += __shfl_xor_sync(0xffffffffu, za, k);
+        }
         if (!GRAD) {  // the slots are free again
           __syncwarp();
           if (lane < C) arrive_remote(map_rank(smem_u32(&result[par]), lane));
@@ -765,9 +846,103 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
     __syncwarp();
   } else {
     // ----------------------------------------------------------- consumers
-    int slot = 0;
+    int slot = 0;        // the next stage of the ring's order
     uint32_t phase = 0;
+    int held = 0;        // resident: the first stage still held
     uint32_t count = 0;  // rows folded
+    // A folded row whose gradient is still to be written.
+    struct Pending {
+      int row, token;
+      float c2, m;
+      bool deep;
+    } last{-1, 0, 0.f, 0.f, false};
+
+    // The token's place in this CTA's share: this thread's granule (counted
+    // along its own granules, -1: another thread's) and element.
+    auto place = [&](const RowShare& sh, int token, int& el) {
+      const int at = token + sh.shift, ag = at / kPer - sh.g0;
+      el = at & (kPer - 1);
+      return token < p.V && ag >= 0 && ag < sh.n && (ag & (kT - 1)) == tid ? ag / kT : -1;
+    };
+    auto grad_image = [&](int row, const RowShare& sh) {
+      return static_cast<char*>(p.d_logits) + (int64_t)row * p.ldd * kB - sh.shift * kB;
+    };
+
+    // Pass 2: a folded row's gradient, number `k` of the rows folded.
+    auto write_grad = [&](const Pending& w, uint32_t k) {
+      if (!wait(&result[k % kSlots], (k / kSlots) & 1u)) {
+        ok = false;
+        return;
+      }
+      const RowGrad r =
+          *reinterpret_cast<const RowGrad*>(reinterpret_cast<char*>(grad) + (k % kSlots) * 32);
+      const RowShare sh = row_share<DT>(p.logits, p.ld, w.row, p.V, q.log2C, rank);
+      char* dz = grad_image(w.row, sh);
+      // aligned as the logits, or written element by element
+      const bool dz_vec = ((uintptr_t)dz & 15u) == 0;
+      int el;
+      const int mine = place(sh, w.token, el);
+      const float c2 = w.c2;
+      const uint64_t nM = pack2(-r.M, -r.M), cc = pack2(c2, c2), nl = pack2(-r.l2S, -r.l2S),
+                     A0 = pack2(r.a0, r.a0), A1 = pack2(r.a1, r.a1);
+      const bool deep = w.deep || (ENT && (w.m - r.M) * c2 < -kDeep);
+      int n = sh.n, first = 0, g = sh.g0 + tid;
+      while (n > 0) {
+        if (!q.resident && !wait(&full[slot], phase)) {
+          ok = false;
+          return;
+        }
+        const int at = q.resident ? held : slot;
+        const uint4* st = reinterpret_cast<const uint4*>(ring + (size_t)at * kStageBytes) + tid;
+        // a stage of whole granules without the token, nothing to clamp
+        const bool plain = (kIter - 1) * kT + tid < n && dz_vec && !deep &&
+                           (unsigned)(mine - first) >= (unsigned)kIter && g >= sh.whole0 &&
+                           g + (kIter - 1) * kT < sh.whole1;
+        if (plain) {
+          uint4* out = reinterpret_cast<uint4*>(dz) + g;
+#pragma unroll
+          for (int j = 0; j < kIter; ++j) {
+            float o[kPer];
+            granule_grad<DT, ENT, false>(st[j * kT], nM, cc, nl, A0, A1, o);
+            store_stream(out + j * kT, granule_pack<DT>(o));
+          }
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < kIter && j * kT + tid < n; ++j) {
+            const int gj = g + j * kT;
+            float o[kPer];
+            granule_grad<DT, ENT, true>(st[j * kT], nM, cc, nl, A0, A1, o);
+            if (first + j == mine) {
+#pragma unroll
+              for (int k = 0; k < kPer; ++k)
+                if (k == el) o[k] = r.own;
+            }
+            if (dz_vec && gj >= sh.whole0 && gj < sh.whole1) {
+              store_stream(reinterpret_cast<uint4*>(dz) + gj, granule_pack<DT>(o));
+            } else {
+#pragma unroll
+              for (int k = 0; k < kPer; ++k) {
+                const int v = gj * kPer + k - sh.shift;
+                if (v >= 0 && v < p.V) store_grad<DT>(dz, (int64_t)gj * kPer + k, o[k]);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[at]);
+        first += kIter;
+        g += kIter * kT;
+        n -= kStageGran;
+        const int next = at + 1 == q.stages ? 0 : at + 1;
+        if (q.resident) {
+          held = next;
+        } else {
+          slot = next;
+          if (next == 0) phase ^= 1u;
+        }
+      }
+    };
+
     int i = cid;
     int token = -1;
     float weight = 1.f, T = p.temp;
@@ -786,15 +961,11 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
         if (p.weights) weight = p.weights[row_of(i + ncl)];
         if (p.temps) T = p.temps[row_of(i + ncl)];
       }
-      const RowShare sh = row_share<DT>(p.logits, p.ld, row, p.V, C, rank);
-      char* dz = nullptr;  // the gradient's image, aligned as the logits' (or element by element)
-      bool dz_vec = false;
-      if (GRAD) {
-        dz = static_cast<char*>(p.d_logits) + (int64_t)row * p.ldd * kB - sh.shift * kB;
-        dz_vec = ((uintptr_t)dz & 15u) == 0;
-      }
+      const RowShare sh = row_share<DT>(p.logits, p.ld, row, p.V, q.log2C, rank);
       if (!live(row, a, wt)) {
-        if (GRAD)
+        if (GRAD) {
+          char* dz = grad_image(row, sh);
+          const bool dz_vec = ((uintptr_t)dz & 15u) == 0;
           for (int g = sh.g0 + tid; g < sh.g0 + sh.n; g += kT) {
             if (dz_vec && g >= sh.whole0 && g < sh.whole1) {
               *reinterpret_cast<uint4*>(dz + (int64_t)g * 16) = make_uint4(0, 0, 0, 0);
@@ -806,14 +977,11 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
               }
             }
           }
+        }
         continue;
       }
-      // the token's place: this thread's granule `mine` (counted along its own
-      // granules), element `el`
-      int mine = -1;
-      const int at = a + sh.shift, ag = at / kPer - sh.g0, el = at & (kPer - 1);
-      const bool here = a < p.V && ag >= 0 && ag < sh.n;
-      if (here && (ag & (kT - 1)) == tid) mine = ag / kT;
+      int el;
+      const int mine = place(sh, a, el);
 
       // pass 1: the sums
       ThreadSums s;
@@ -821,7 +989,6 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
       s.R[0] = s.R[1] = s.Q[0] = s.Q[1] = 0ull;
       bool deep = false;
       float za = 0.f;
-      const int slot0 = slot;
       int n = sh.n;   // granules left
       int first = 0;  // the stage's first granule of this thread
       while (n > 0) {
@@ -832,22 +999,33 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
         const uint4* st = reinterpret_cast<const uint4*>(ring + (size_t)slot * kStageBytes) + tid;
         const int drop =
             (unsigned)(mine - first) < (unsigned)kIter ? (mine - first) * kPer + el : -1;
-        if (n >= kStageGran) {
+        unsigned low = 0u;
+        const int g = sh.g0 + first * kT + tid;
+        if ((kIter - 1) * kT + tid < n) {
           uint4 w[kIter];
 #pragma unroll
           for (int j = 0; j < kIter; ++j) w[j] = st[j * kT];
-          fold<DT, ENT, kIter>(s, w, st, kT, drop, c2, sh.g0 + first * kT + tid, sh.whole0,
-                               sh.whole1, za, deep);
+          fold<DT, ENT, kIter>(s, w, drop, c2, za, low);
         } else {
-          // the share's last granules, one at a time
+          // past the share's end: what is left, one granule at a time
 #pragma unroll 1
-          for (int j = 0; j < kIter && j * kT + tid < n; ++j) {
-            const uint4 w[1] = {st[j * kT]};
-            const int dj = drop >= j * kPer && drop < (j + 1) * kPer ? drop - j * kPer : -1;
-            fold<DT, ENT, 1>(s, w, st + j * kT, kT, dj, c2, sh.g0 + (first + j) * kT + tid,
-                             sh.whole0, sh.whole1, za, deep);
+          for (int j = 0; j < kIter - 1 && j * kT + tid < n; ++j) {
+            uint4 w[1] = {st[j * kT]};
+            unsigned l = 0u;
+            fold<DT, ENT, 1>(s, w, drop >= j * kPer && drop < (j + 1) * kPer ? drop - j * kPer : -1,
+                             c2, za, l);
+            low |= l << j;
           }
-          __syncwarp();
+        }
+        // Elements far below the reference need the clamp again for their
+        // gradient.  The granules that the row fills in part and the token's
+        // own have it anyway.
+        if (GRAD && low) {
+#pragma unroll
+          for (int j = 0; j < kIter; ++j)
+            if ((low >> j & 1u) && first + j != mine && g + j * kT >= sh.whole0 &&
+                g + j * kT < sh.whole1)
+              deep = true;
         }
         if (!GRAD || !q.resident) {
           __syncwarp();
@@ -863,14 +1041,15 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
       if (!ok) break;
       // this warp's sums to the finishing CTAs, with the token's logit where
       // this warp holds it
-      const uint32_t par = count & 1u;
+      const uint32_t par = count % kSlots;
       const RowSums rs = warp_join(RowSums{s.m, pair_sum(s.R), ENT ? pair_sum(s.Q) : 0.f}, c2);
-      const int holder = here ? ag & (kT - 1) : -1;
-      za = __shfl_sync(0xffffffffu, za, holder & 31);
-      if (!here || (holder >> 5) != warp) za = 0.f;
-      // without a gradient nothing else holds this warp back: the slots must
-      // have been read two rows ago
-      if (!GRAD && count >= 2 && !wait(&result[par], ((count >> 1) - 1u) & 1u)) {
+      const unsigned holder = __ballot_sync(0xffffffffu, mine >= 0);
+      za = holder ? __shfl_sync(0xffffffffu, za, __ffs(holder) - 1) : 0.f;
+      // A slot's last sums have been read.  Without a gradient the first CTA's
+      // finisher says so.  With one it follows: a CTA sends row k + kSlots
+      // after its result of row k + 2, which needed this CTA's sums of row
+      // k + 2, sent after this CTA's result of row k.
+      if (!GRAD && count >= kSlots && !wait(&result[par], (count / kSlots - 1u) & 1u)) {
         ok = false;
         break;
       }
@@ -879,86 +1058,18 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
         st_async4(map_rank(to, lane), rs.m, rs.R, rs.Q, za,
                   map_rank(smem_u32(&sums_in[par]), lane));
       }
+      if (GRAD) {
+        const Pending now{row, a, c2, s.m, deep};
+        if (!q.ahead)
+          write_grad(now, count);
+        else if (last.row >= 0)
+          write_grad(last, count - 1u);
+        if (!ok) break;
+        last = now;
+      }
       ++count;
-      if (!GRAD) continue;
-
-      // pass 2: the gradient, from the stages that still hold the row
-      if (!wait(&result[par], ((count - 1u) >> 1) & 1u)) {
-        ok = false;
-        break;
-      }
-      const RowGrad r = *reinterpret_cast<const RowGrad*>(reinterpret_cast<char*>(grad) + par * 32);
-      const uint64_t nM = pack2(-r.M, -r.M), cc = pack2(c2, c2), nl = pack2(-r.l2S, -r.l2S),
-                     A0 = pack2(r.a0, r.a0), A1 = pack2(r.a1, r.a1);
-      if (ENT && (s.m - r.M) * c2 < -kDeep) deep = true;
-      if (q.resident) slot = slot0;
-      n = sh.n;
-      first = 0;
-      int g = sh.g0 + tid;
-      while (n > 0) {
-        if (!q.resident && !wait(&full[slot], phase)) {
-          ok = false;
-          break;
-        }
-        const uint4* st = reinterpret_cast<const uint4*>(ring + (size_t)slot * kStageBytes) + tid;
-        auto granule_grad = [&](const uint4& raw) {
-          const Granule<DT> z = granule<DT>(raw);
-          float o[kPer];
-#pragma unroll
-          for (int k = 0; k < kPer / 2; ++k) {
-            const uint64_t x = fma2(add2(z.v[k], nM), cc, nl);
-            float xa, xb;
-            unpack2(x, xa, xb);
-            const uint64_t e = pack2(ex2(xa), ex2(xb));
-            unpack2(mul2(e, ENT ? fma2(A1, x, A0) : A0), o[2 * k], o[2 * k + 1]);
-          }
-          if constexpr (DT == kScoreF32)
-            return make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]),
-                              __float_as_uint(o[3]));
-          else
-            return make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
-                              pack_bf16(o[6], o[7]));
-        };
-        // a stage of whole granules without the token, nothing to clamp
-        const bool plain = n >= kStageGran && dz_vec && !deep &&
-                           (unsigned)(mine - first) >= (unsigned)kIter && g >= sh.whole0 &&
-                           g + (kIter - 1) * kT < sh.whole1;
-        if (plain) {
-          uint4* out = reinterpret_cast<uint4*>(dz) + g;
-#pragma unroll
-          for (int j = 0; j < kIter; ++j) out[j * kT] = granule_grad(st[j * kT]);
-        } else {
-#pragma unroll 1
-          for (int j = 0; j < kIter && j * kT + tid < n; ++j) {
-            const int gj = g + j * kT;
-            if (!deep && first + j != mine && dz_vec && gj >= sh.whole0 && gj < sh.whole1) {
-              reinterpret_cast<uint4*>(dz)[gj] = granule_grad(st[j * kT]);
-              continue;
-            }
-#pragma unroll 1
-            for (int k = 0; k < kPer; ++k) {
-              const int v = gj * kPer + k - sh.shift;
-              if (v < 0 || v >= p.V) continue;
-              float x = (load_logit<DT>(st + j * kT, k) - r.M) * c2;
-              if (ENT) x = x < -kDeep ? -kDeep : x;
-              x -= r.l2S;
-              const float o = ex2(x) * (ENT ? fmaf(r.a1, x, r.a0) : r.a0);
-              store_grad<DT>(dz, (int64_t)gj * kPer + k,
-                             first + j == mine && k == el ? r.own : o);
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[slot]);
-        first += kIter;
-        g += kIter * kT;
-        n -= kStageGran;
-        if (++slot == q.stages) {
-          slot = 0;
-          if (!q.resident) phase ^= 1u;
-        }
-      }
     }
+    if (GRAD && ok && q.ahead && last.row >= 0) write_grad(last, count - 1u);
     if (!ok) {
       if (lane == 0) fail();
       // sums of this row may still be on their way to other CTAs: they land
