@@ -25,43 +25,42 @@ using ebk::align256;
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int kMaxGrid = 2048;  // CTAs of a policy launch (partial sums kept for each)
+constexpr int kMaxGrid = 8192;  // partial sums of a policy launch
 
-// The row kernel's variants: [bf16][entropy][gradient][wide].
-template <int DT, bool ENT, bool GRAD, int NW>
+// The row kernels' variants: [bf16][entropy][gradient].
+constexpr int kVariants = 8;
+template <int DT, bool ENT, bool GRAD>
 const void* ring_fn() {
-  return reinterpret_cast<const void*>(&ebk::score_ring_kernel<DT, ENT, GRAD, NW>);
+  return reinterpret_cast<const void*>(&ebk::score_ring_kernel<DT, ENT, GRAD>);
 }
-constexpr int kRingVariants = 16;
-const void* const kRing[kRingVariants] = {
-    ring_fn<ebk::kScoreF32, false, false, 4>(),  ring_fn<ebk::kScoreF32, false, false, 8>(),
-    ring_fn<ebk::kScoreF32, false, true, 4>(),   ring_fn<ebk::kScoreF32, false, true, 8>(),
-    ring_fn<ebk::kScoreF32, true, false, 4>(),   ring_fn<ebk::kScoreF32, true, false, 8>(),
-    ring_fn<ebk::kScoreF32, true, true, 4>(),    ring_fn<ebk::kScoreF32, true, true, 8>(),
-    ring_fn<ebk::kScoreBF16, false, false, 4>(), ring_fn<ebk::kScoreBF16, false, false, 8>(),
-    ring_fn<ebk::kScoreBF16, false, true, 4>(),  ring_fn<ebk::kScoreBF16, false, true, 8>(),
-    ring_fn<ebk::kScoreBF16, true, false, 4>(),  ring_fn<ebk::kScoreBF16, true, false, 8>(),
-    ring_fn<ebk::kScoreBF16, true, true, 4>(),   ring_fn<ebk::kScoreBF16, true, true, 8>()};
-int ring_variant(bool bf16, bool ent, bool grad, bool wide) {
-  return (bf16 ? 8 : 0) + (ent ? 4 : 0) + (grad ? 2 : 0) + (wide ? 1 : 0);
+const void* const kRing[kVariants] = {
+    ring_fn<ebk::kScoreF32, false, false>(),  ring_fn<ebk::kScoreF32, false, true>(),
+    ring_fn<ebk::kScoreF32, true, false>(),   ring_fn<ebk::kScoreF32, true, true>(),
+    ring_fn<ebk::kScoreBF16, false, false>(), ring_fn<ebk::kScoreBF16, false, true>(),
+    ring_fn<ebk::kScoreBF16, true, false>(),  ring_fn<ebk::kScoreBF16, true, true>()};
+template <int DT, bool ENT, bool GRAD, int W>
+const void* short_fn() {
+  return reinterpret_cast<const void*>(&ebk::score_short_kernel<DT, ENT, GRAD, W>);
 }
+const void* const kShort[2][kVariants] = {
+    {short_fn<ebk::kScoreF32, false, false, 1>(), short_fn<ebk::kScoreF32, false, true, 1>(),
+     short_fn<ebk::kScoreF32, true, false, 1>(), short_fn<ebk::kScoreF32, true, true, 1>(),
+     short_fn<ebk::kScoreBF16, false, false, 1>(), short_fn<ebk::kScoreBF16, false, true, 1>(),
+     short_fn<ebk::kScoreBF16, true, false, 1>(), short_fn<ebk::kScoreBF16, true, true, 1>()},
+    {short_fn<ebk::kScoreF32, false, false, 4>(), short_fn<ebk::kScoreF32, false, true, 4>(),
+     short_fn<ebk::kScoreF32, true, false, 4>(), short_fn<ebk::kScoreF32, true, true, 4>(),
+     short_fn<ebk::kScoreBF16, false, false, 4>(), short_fn<ebk::kScoreBF16, false, true, 4>(),
+     short_fn<ebk::kScoreBF16, true, false, 4>(), short_fn<ebk::kScoreBF16, true, true, 4>()}};
 
-// Two wide CTAs (6 stages of 16 KB) or four narrow ones (4 stages of 8 KB)
-// share an SM.
-constexpr int kWideStages = 6, kNarrowStages = 4;
-size_t ring_smem_of(bool wide) {
-  return wide ? ebk::ring_layout(kWideStages, 8).total : ebk::ring_layout(kNarrowStages, 4).total;
-}
-constexpr int64_t kNarrowBytes = 16384;  // rows up to this take the narrow form
-constexpr int kShareStages = 4;          // a wide CTA's share where the cluster allows it
-constexpr int kMaxLog2C = 3;
+constexpr int kRingStages = 6;  // two CTAs of 96 KB rings share an SM
+constexpr int kMaxLog2C = 4;
 
 struct DeviceInfo {
   std::once_flag once;
   int rc = EB_ERR_CUDA;
   int sms = 0;
   size_t optin = 0;
-  std::atomic<int> clusters[kRingVariants][5];
+  std::atomic<int> clusters[kVariants][kMaxLog2C + 1];  // that fit at once, plus 1; 0: not asked
 };
 DeviceInfo g_info[kMaxDevices];
 
@@ -85,19 +84,20 @@ void info_setup(DeviceInfo& d, int device) {
     d.rc = EB_ERR_CUDA;
     return;
   }
-  for (int v = 0; v < kRingVariants; ++v) {
-    const size_t smem = ring_smem_of(v & 1);
-    if (smem > (size_t)optin) {
-      d.rc = EB_ERR_UNSUPPORTED;
-      return;
-    }
-    if (cudaFuncSetAttribute(kRing[v], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess) {
+  const uint32_t ring_smem = ebk::ring_layout(kRingStages).total;
+  if (ring_smem > (uint32_t)optin) {
+    d.rc = EB_ERR_UNSUPPORTED;
+    return;
+  }
+  for (int v = 0; v < kVariants; ++v)
+    if (cudaFuncSetAttribute(kRing[v], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)ring_smem) != cudaSuccess ||
+        cudaFuncSetAttribute(kRing[v], cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+            cudaSuccess) {
       cudaGetLastError();
       d.rc = EB_ERR_CUDA;
       return;
     }
-  }
   d.sms = sms;
   d.optin = (size_t)optin;
   d.rc = EB_OK;
@@ -164,76 +164,125 @@ void fill_args(const eb_scorer* h, const eb_score_input_t* in, ScoreArgs& a) {
   a.wait_ns = h->wait_ns;
 }
 
-// How a launch over rows is laid out.
-struct RingPlan {
-  int wide;      // 8 consumer warps and a large ring, else 4 and a small one
-  int log2C;     // CTAs per row
-  int resident;  // a row's stages are kept until its gradient
-  int ahead;     // the next row is folded before this one's gradient
-};
-
-int share_stages(int64_t row_bytes, int C, int warps) {
-  const int gran = ebk::stage_bytes(warps) / 16;
-  // the aligned image of a row spans up to one granule more than its bytes
-  const int64_t G = (row_bytes + 15) / 16 + 1;
-  const int64_t per = ((G + C - 1) / C + 7) / 8 * 8;
-  return (int)std::min<int64_t>((per + gran - 1) / gran, 1 << 20);
+void ring_config(cudaLaunchConfig_t& lc, cudaLaunchAttribute& attr, int clusters, int log2C,
+                 cudaStream_t st) {
+  std::memset(&lc, 0, sizeof(lc));
+  lc.gridDim = dim3((unsigned)clusters << log2C);
+  lc.blockDim = dim3(ebk::kRingThreads);
+  lc.dynamicSmemBytes = ebk::ring_layout(kRingStages).total;
+  lc.stream = st;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 1u << log2C;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  lc.attrs = &attr;
+  lc.numAttrs = 1;
 }
 
-RingPlan ring_plan(int sms, int64_t rows, int64_t row_bytes) {
-  RingPlan r;
-  r.wide = row_bytes > kNarrowBytes;
-  r.log2C = 0;
-  const int warps = r.wide ? 8 : 4, stages = r.wide ? kWideStages : kNarrowStages;
-  if (r.wide) {
-    while (r.log2C < kMaxLog2C && share_stages(row_bytes, 1 << r.log2C, 8) > kShareStages)
-      ++r.log2C;
-    while (r.log2C < kMaxLog2C && (rows << (r.log2C + 1)) <= 2 * sms &&
-           (row_bytes >> r.log2C) > ebk::stage_bytes(8))
-      ++r.log2C;
+// Clusters of 2^log2C ring CTAs that fit the device at once (the current
+// one), asked once per variant and size; 0: none.
+int ring_clusters(int device, int variant, int log2C) {
+  std::atomic<int>& cached = g_info[device].clusters[variant][log2C];
+  const int known = cached.load(std::memory_order_relaxed);
+  if (known > 0) return known - 1;
+  cudaLaunchConfig_t lc;
+  cudaLaunchAttribute attr;
+  ring_config(lc, attr, 1, log2C, nullptr);
+  int most = 0;
+  if (cudaOccupancyMaxActiveClusters(&most, kRing[variant], &lc) != cudaSuccess) {
+    cudaGetLastError();
+    most = 0;
   }
-  const int share = share_stages(row_bytes, 1 << r.log2C, warps);
-  r.resident = 2 * share <= stages;
-  r.ahead = 1;
-  return r;
+  most = std::max(0, std::min(most, kMaxGrid));
+  cached.store(most + 1, std::memory_order_relaxed);
+  return most;
+}
+
+int share_stages(int64_t row_bytes, int log2C) {
+  // the aligned image of a row spans up to one granule more than its bytes
+  const int64_t G = (row_bytes + 15) / 16 + 1;
+  const int64_t per = (((G + (1ll << log2C) - 1) >> log2C) + 7) / 8 * 8;
+  return (int)std::min<int64_t>((per + ebk::kStageGran - 1) / ebk::kStageGran, 1 << 20);
+}
+
+// The cluster size of a ring launch.  A row on 2^c CTAs costs a CTA its share
+// of the row at the CTA's rate, and about a microsecond more for the exchange;
+// rows go in waves of the clusters that fit.  More CTAs per row shorten the
+// last, partly filled wave and (with a gradient, whose second look at a row
+// should find it in L2) keep fewer rows in flight; fewer pay the exchange less
+// often.  The rates are what one CTA was measured to take, in KB/us: alone on
+// its SM, and with every SM holding two.  Measured both ways, 262144 bf16:
+// one row, forward, 22.6 us on one CTA and 5.5 on 16; 600 rows, with gradient,
+// 161 us on one CTA each, 134 on two, 170 on eight.
+int ring_log2C(const eb_scorer* h, int variant, bool f32, bool grad, int64_t rows,
+               int64_t row_bytes) {
+  const double alone = (grad ? 13.0 : 26.0) * (f32 ? 1.4 : 1.0);
+  const double full = (grad ? 9.3 : 18.0) * (f32 ? 1.25 : 1.0);
+  const double kb = (double)row_bytes / 1024.0;
+  int best = 0;
+  double best_t = 0.0;
+  for (int c = 0; c <= kMaxLog2C; ++c) {
+    const int n = ring_clusters(h->device, variant, c);
+    if (n < 1) break;
+    const double share = kb / (1 << c), fixed = (grad ? 1.4 : 1.1) + 0.1 * c;
+    // the part of a share that the ring does not keep is copied again, from
+    // L2, or from HBM where more rows are in flight than L2 keeps
+    const double flight = (double)std::min<int64_t>(n, rows) * kb / 1024.0;
+    const int stages = share_stages(row_bytes, c);
+    const double over = std::min(1.0, std::max(0.0, (flight - 40.0) / 100.0));
+    const double again =
+        grad && stages > kRingStages
+            ? 1.0 + (1.0 - (double)kRingStages / stages) * (0.3 + 0.3 * over)
+            : 1.0;
+    const int64_t waves = rows / n, left = rows - waves * n;
+    double t = (double)waves * (fixed + share / full * again);
+    if (left > 0) {
+      const double ctas = (double)(left << c);
+      const double crowd = std::min(1.0, std::max(0.0, (ctas - h->sms) / (double)h->sms));
+      t += fixed + share / (alone + (full - alone) * crowd) * again;
+    }
+    if (c == 0 || t < best_t) {
+      best = c;
+      best_t = t;
+    }
+  }
+  return best;
 }
 
 int launch_rows(const eb_scorer* h, const ScoreArgs& a, int dtype, int mode, bool ent, bool grad,
                 bool reverse, cudaStream_t st) {
-  const RingPlan r = ring_plan(h->sms, a.rows, (int64_t)a.V * (int64_t)elt_bytes(dtype));
-  const int v = ring_variant(dtype == EB_BF16, ent, grad, r.wide);
-  const int warps = r.wide ? 8 : 4;
+  const int v = (dtype == EB_BF16 ? 4 : 0) + (ent ? 2 : 0) + (grad ? 1 : 0);
+  const int64_t row_bytes = (int64_t)a.V * (int64_t)elt_bytes(dtype);
+  // the aligned image of a row holds a granule more where rows start off 16 bytes
+  const bool even = (uintptr_t)a.logits % 16 == 0 && (a.ld * (int64_t)elt_bytes(dtype)) % 16 == 0;
+  const int64_t image = (row_bytes + 15) / 16 * 16 + (even ? 0 : 16);
+  if (image <= ebk::short_bytes(4)) {
+    // four warps to a row also where one would do but every row has its SM's
+    // attention anyway (16 rows of 1024 fp32: 2.1 us against 2.8; 2000: 6.8
+    // against 4.6)
+    const int wide = image > ebk::short_bytes(1) || (image > 1024 && a.rows <= 4 * h->sms);
+    const int per_block = wide ? 1 : 4;
+    const int blocks = (int)std::min<int64_t>(((int64_t)a.rows + per_block - 1) / per_block,
+                                              (int64_t)h->sms * (grad ? 6 : 8));
+    int m = mode, r = reverse ? 1 : 0;
+    void* args[] = {const_cast<ScoreArgs*>(&a), &m, &r};
+    return cudaLaunchKernel(kShort[wide][v], dim3(std::max(1, blocks)), dim3(ebk::kShortThreads),
+                            args, 0, st) == cudaSuccess
+               ? EB_OK
+               : EB_ERR_CUDA;
+  }
+  const int c = ring_log2C(h, v, dtype == EB_F32, grad, a.rows, row_bytes);
+  const int most = ring_clusters(h->device, v, c);
+  if (most < 1) return EB_ERR_CUDA;
   ebk::RingArgs q;
   q.mode = mode;
   q.reverse = reverse ? 1 : 0;
-  q.log2C = r.log2C;
-  q.stages = r.wide ? kWideStages : kNarrowStages;
-  q.resident = r.resident;
-  q.ahead = r.ahead;
+  q.log2C = c;
+  q.stages = kRingStages;
+  q.ahead = 2 * share_stages(row_bytes, c) <= kRingStages;
+  q.keep = kRingStages;
   cudaLaunchConfig_t lc;
-  std::memset(&lc, 0, sizeof(lc));
-  lc.blockDim = dim3((warps + 2) * 32);
-  lc.dynamicSmemBytes = ring_smem_of(r.wide);
-  lc.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1 << r.log2C;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  // the clusters that fit the device at once, asked once per variant and size
-  std::atomic<int>& cached = g_info[h->device].clusters[v][r.log2C];
-  int most = cached.load(std::memory_order_relaxed);
-  if (most == 0) {
-    lc.gridDim = dim3(1 << r.log2C);
-    if (cudaOccupancyMaxActiveClusters(&most, kRing[v], &lc) != cudaSuccess || most < 1) {
-      cudaGetLastError();
-      return EB_ERR_CUDA;
-    }
-    most = std::min(most, kMaxGrid);
-    cached.store(most, std::memory_order_relaxed);
-  }
-  lc.gridDim = dim3(std::max(1, std::min(a.rows, most)) << r.log2C);
+  cudaLaunchAttribute attr;
+  ring_config(lc, attr, std::max(1, std::min(a.rows, most)), c, st);
   void* args[] = {const_cast<ScoreArgs*>(&a), &q};
   return cudaLaunchKernelExC(&lc, kRing[v], args) == cudaSuccess ? EB_OK : EB_ERR_CUDA;
 }

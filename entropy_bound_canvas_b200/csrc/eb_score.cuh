@@ -176,6 +176,40 @@ struct RowCoef {
   float g, h;  // upstream gradients of log p_a and H
 };
 
+// What a row's gradient is made from.
+struct RowGrad {
+  float M, l2S;  // p = 2^((z - M) c2 - l2S)
+  float a0, a1;  // gradient p (a0 + a1 log2 p)
+  float own;     // the token's element
+};
+
+template <bool ENT>
+__device__ __forceinline__ RowGrad row_grad(const RowResult& r, RowCoef c, float T) {
+  const float iT = 1.f / T;
+  RowGrad o;
+  o.M = r.M;
+  o.l2S = r.l2S;
+  o.a0 = -iT * (ENT ? fmaf(c.h, r.H, c.g) : c.g);
+  o.a1 = -iT * c.h * kLn2;
+  // p_a = 0: log p_a may be -inf, its entropy term is 0
+  const float ha = !ENT ? 0.f : r.pa > 0.f ? c.h * r.pa * (r.lp + r.H) : r.pa;
+  o.own = iT * (c.g * r.rest - ha);
+  return o;
+}
+
+// The rows that count: those of the sequences, where there are any.
+struct RowRange {
+  int lo, hi;
+  __device__ __forceinline__ bool live(int row, int token, float weight) const {
+    return token >= 0 && weight != 0.f && row >= lo && row < hi;
+  }
+};
+__device__ __forceinline__ RowRange row_range(const ScoreArgs& p) {
+  RowRange r{0, p.rows};
+  if (p.offsets) r = RowRange{p.offsets[0], p.offsets[p.n_off]};
+  return r;
+}
+
 // The policy loss of a row: its gradients, and its terms added to t.
 //   L = w [ max(-A r, -A clip(r)) + k KL - c H ],  r = exp(log p_a - old),
 //   KL = exp(ref - log p_a) - 1 - (ref - log p_a)
@@ -210,25 +244,50 @@ __device__ __forceinline__ RowCoef policy_row(const ScoreArgs& p, const RowResul
   return c;
 }
 
-// The last of n CTAs to arrive sums the parts, in an order of its own that
-// does not depend on who arrived when: the same bits at every launch of one
-// grid.  Called by one whole block each, after its part was written.
-template <int WARPS>
-__device__ __forceinline__ void policy_total(const ScoreArgs& p, int n) {
+// The loss's terms.  A CTA's part is the sum of its leaders' t (one thread
+// each, numbered from 0); the last of n CTAs to arrive sums the parts, in an
+// order of its own that does not depend on who arrived when: the same bits at
+// every launch of one grid.  Called by whole blocks, this one being `index`.
+template <int THREADS, int LEADERS>
+__device__ __forceinline__ void policy_total(const ScoreArgs& p, int leader,
+                                             const double (&t)[kPolicyTerms], int index, int n) {
+  constexpr int kWarps = THREADS / 32;
+  __shared__ double sums[kWarps][kPolicyTerms];
   __shared__ int last;
+  if (leader >= 0)
+    for (int k = 0; k < kPolicyTerms; ++k) sums[leader][k] = t[k];
+  __syncthreads();
   if (threadIdx.x == 0) {
-    const int old = atom_add_acq_rel_gpu(reinterpret_cast<int*>(p.counter), 1);
-    last = old == n - 1;
-    if (last) *p.counter = 0u;
+    for (int k = 0; k < kPolicyTerms; ++k) {
+      double v = 0.0;
+      for (int w = 0; w < LEADERS; ++w) v += sums[w][k];
+      if (n > 1)
+        p.part[(size_t)index * kPolicyTerms + k] = v;
+      else
+        p.terms[k] = (float)v;
+    }
+    last = 0;
+    if (n > 1) {
+      last = atom_add_acq_rel_gpu(reinterpret_cast<int*>(p.counter), 1) == n - 1;
+      if (last) *p.counter = 0u;
+    }
   }
   __syncthreads();
   if (!last) return;
-  const int lane = threadIdx.x & 31;
-  for (int k = threadIdx.x >> 5; k < kPolicyTerms; k += WARPS) {
-    double s = 0.0;
-    for (int i = lane; i < n; i += 32) s += __ldcg(p.part + (size_t)i * kPolicyTerms + k);
-    for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-    if (lane == 0) p.terms[k] = (float)s;
+  double s[kPolicyTerms] = {};
+  for (int i = threadIdx.x; i < n; i += THREADS)
+#pragma unroll
+    for (int k = 0; k < kPolicyTerms; ++k) s[k] += __ldcg(p.part + (size_t)i * kPolicyTerms + k);
+#pragma unroll
+  for (int k = 0; k < kPolicyTerms; ++k)
+    for (int m = 16; m > 0; m >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], m);
+  if ((threadIdx.x & 31) == 0)
+    for (int k = 0; k < kPolicyTerms; ++k) sums[threadIdx.x >> 5][k] = s[k];
+  __syncthreads();
+  if (threadIdx.x < kPolicyTerms) {
+    double v = 0.0;
+    for (int w = 0; w < kWarps; ++w) v += sums[w][threadIdx.x];
+    p.terms[threadIdx.x] = (float)v;
   }
 }
 
@@ -246,20 +305,27 @@ __device__ __forceinline__ void policy_total(const ScoreArgs& p, int n) {
 //              computes the row's results and its gradient's factors.
 // Without a gradient only the first CTA finishes, and the consumers go on to
 // the next row at once.  With one every CTA does (the same arithmetic, the
-// same bits), and the consumers fold the next row before they turn this one
-// into its gradient, so that the exchange and the finisher's work run under
-// that.  Where two shares fit the ring (resident) a row's stages are kept
-// until then.  Otherwise its share is copied a second time, from L2: a row
-// per cluster, two in flight, stay there (the first copy asks for it).
+// same bits), and the consumers turn what the ring holds into the gradient:
+//   ahead      where two shares fit the ring, they fold the next row first, so
+//              that the exchange and the finisher's work run under that;
+//   otherwise  they go through the share a second time in the opposite order.
+//              Its last stages are still in the ring; the others are copied
+//              again, the most recent first, so that most come from L2 (the
+//              first copy asks L2 to keep them).
 //
 // Rows start at any element.  A share is a range of 16-byte granules of the
 // row's 16-byte-aligned image; the granules that the row fills only partly
 // (at its two ends) are gathered element by element, with -inf in the places
 // that are not the row's, and stored element by element.
 // ---------------------------------------------------------------------------
+constexpr int kRingWarps = 8;  // consumers
+constexpr int kRingThreads = (kRingWarps + 2) * 32;
+constexpr int kRingCtas = 2;   // per SM
 constexpr int kStageIter = 4;  // granules of a stage per consumer thread
-constexpr __host__ __device__ int stage_bytes(int warps) { return warps * 32 * 16 * kStageIter; }
+constexpr int kStageGran = kRingWarps * 32 * kStageIter;
+constexpr int kStageBytes = kStageGran * 16;
 constexpr int kMaxCluster = 16;
+
 // A thread moves its reference to a new maximum only when that exceeds it by
 // 2^kLazy: a row that one logit dominates still has that logit as its
 // reference (any other is over 2^kLazy below it), and the others' sums are as
@@ -270,25 +336,37 @@ struct RingArgs {
   int mode, reverse;
   int log2C;     // CTAs per cluster: a power of two
   int stages;    // of the ring
-  int resident;  // rows are kept in the ring until their gradient: copied once
-  int ahead;     // the next row is folded before this one's gradient (resident: two shares fit)
+  int ahead;     // two shares fit: the next row is folded before this one's gradient
+  int keep;      // not ahead: the share's last stages kept for the gradient
+};
+
+// The ring's slots in their order of use, the same for the producer and the
+// consumers, each slot with the parity of its next wait.
+struct RingWalk {
+  int slot, dir, stages;
+  uint32_t parity;  // by slot
+  __device__ __forceinline__ uint32_t phase() const { return parity >> slot & 1u; }
+  __device__ __forceinline__ void used() { parity ^= 1u << slot; }
+  __device__ __forceinline__ void step(int n = 1) {
+    slot += dir * n;
+    if (slot >= stages) slot -= stages;
+    if (slot < 0) slot += stages;
+  }
+  // The next slot is the one used last.
+  __device__ __forceinline__ void turn() {
+    dir = -dir;
+    step();
+  }
 };
 constexpr int kSlots = 4;  // rows between a slot's uses, see the kernel
-
-// What the consumers need for a row's gradient.
-struct RowGrad {
-  float M, l2S;  // p = 2^((z - M) c2 - l2S)
-  float a0, a1;  // gradient p (a0 + a1 log2 p)
-  float own;     // the token's element
-};
 
 struct RingLayout {
   uint32_t part, grad, bars, flag, total;
 };
-__host__ __device__ constexpr RingLayout ring_layout(int stages, int warps) {
+__host__ __device__ constexpr RingLayout ring_layout(int stages) {
   RingLayout y{};
-  y.part = (uint32_t)(stages * stage_bytes(warps));
-  y.grad = y.part + (uint32_t)(kSlots * kMaxCluster * warps * 16);
+  y.part = (uint32_t)(stages * kStageBytes);
+  y.grad = y.part + (uint32_t)(kSlots * kMaxCluster * kRingWarps * 16);
   y.bars = y.grad + kSlots * 32u;
   y.flag = y.bars + (2u * (uint32_t)stages + 2u * kSlots) * 8u;
   y.total = y.flag + 16u;
@@ -361,23 +439,34 @@ __device__ __forceinline__ void store_stream(uint4* p, const uint4& v) {
   __stcs(p, v);
 }
 
-// One granule of 16 bytes as packed fp32 pairs.
+// The two bf16 of a word minus m, in fp32.
+__device__ __forceinline__ uint64_t bf_minus(uint32_t w, float m) {
+  float lo, hi;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tsub.f32.bf16 %0, l, %3;\n\t"
+      "sub.f32.bf16 %1, h, %3;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(w), "f"(m));
+  return pack2(lo, hi);
+}
+
+// One granule of 16 bytes, minus m, as packed fp32 pairs.
 template <int DT>
 struct Granule {
   static constexpr int kPairs = ScoreType<DT>::kPer16 / 2;
   uint64_t v[kPairs];
 };
 template <int DT>
-__device__ __forceinline__ Granule<DT> granule(const uint4& w) {
+__device__ __forceinline__ Granule<DT> granule_minus(const uint4& w, float m) {
   Granule<DT> g;
   if constexpr (DT == kScoreF32) {
-    g.v[0] = pack2(__uint_as_float(w.x), __uint_as_float(w.y));
-    g.v[1] = pack2(__uint_as_float(w.z), __uint_as_float(w.w));
+    const uint64_t nm = pack2(-m, -m);
+    g.v[0] = add2(pack2(__uint_as_float(w.x), __uint_as_float(w.y)), nm);
+    g.v[1] = add2(pack2(__uint_as_float(w.z), __uint_as_float(w.w)), nm);
   } else {
-    g.v[0] = pack2(bf_lo(w.x), bf_hi(w.x));
-    g.v[1] = pack2(bf_lo(w.y), bf_hi(w.y));
-    g.v[2] = pack2(bf_lo(w.z), bf_hi(w.z));
-    g.v[3] = pack2(bf_lo(w.w), bf_hi(w.w));
+    g.v[0] = bf_minus(w.x, m);
+    g.v[1] = bf_minus(w.y, m);
+    g.v[2] = bf_minus(w.z, m);
+    g.v[3] = bf_minus(w.w, m);
   }
   return g;
 }
@@ -448,14 +537,14 @@ __device__ __forceinline__ float pair_sum(const uint64_t (&v)[2]) {
 template <int DT, bool ENT, bool CLAMP, int N>
 __device__ __forceinline__ void granule_sums(const uint4 (&w)[N], float m, float c2,
                                              uint64_t (&R)[2], uint64_t (&Q)[2], unsigned& low) {
-  const uint64_t nm = pack2(-m, -m), cc = pack2(c2, c2);
+  const uint64_t cc = pack2(c2, c2);
   R[0] = R[1] = Q[0] = Q[1] = 0ull;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    const Granule<DT> v = granule<DT>(w[n]);
+    const Granule<DT> v = granule_minus<DT>(w[n], m);
 #pragma unroll
     for (int k = 0; k < Granule<DT>::kPairs; ++k) {
-      uint64_t d = mul2(add2(v.v[k], nm), cc);
+      uint64_t d = mul2(v.v[k], cc);
       float d0, d1;
       unpack2(d, d0, d1);
       if (CLAMP) {  // by comparison, so that NaN stays NaN
@@ -471,6 +560,22 @@ __device__ __forceinline__ void granule_sums(const uint4 (&w)[N], float m, float
   }
 }
 
+// The thread's sums moved to the reference of N granules' maximum, where that
+// is 2^kLazy above theirs or more.
+template <int DT, bool ENT, int N>
+__device__ __forceinline__ void raise(ThreadSums& s, const uint4 (&w)[N], float c2) {
+  const float hi = granule_max<DT, N>(w);
+  if (!((hi - s.m) * c2 > kLazy)) return;  // the empty reference is -FLT_MAX
+  const float d = fmaxf((s.m - hi) * c2, -kDeep), f = ex2(d);
+  const uint64_t f2 = pack2(f, f), d2 = pack2(d, d);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (ENT) s.Q[k] = mul2(f2, fma2(d2, s.R[k], s.Q[k]));
+    s.R[k] = mul2(f2, s.R[k]);
+  }
+  s.m = hi;
+}
+
 // Folds N granules into a thread's sums.  `drop`: the element that is left out
 // (counted through the N granules), or -1; its value goes to `za`.  `low`: the
 // granules with elements so far below the reference that their exponent has
@@ -478,17 +583,7 @@ __device__ __forceinline__ void granule_sums(const uint4 (&w)[N], float m, float
 template <int DT, bool ENT, int N>
 __device__ __forceinline__ void fold(ThreadSums& s, uint4 (&w)[N], int drop, float c2, float& za,
                                      unsigned& low) {
-  const float hi = granule_max<DT, N>(w);
-  if ((hi - s.m) * c2 > kLazy) {  // also from the empty reference -FLT_MAX
-    const float d = fmaxf((s.m - hi) * c2, -kDeep), f = ex2(d);
-    const uint64_t f2 = pack2(f, f), d2 = pack2(d, d);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (ENT) s.Q[k] = mul2(f2, fma2(d2, s.R[k], s.Q[k]));
-      s.R[k] = mul2(f2, s.R[k]);
-    }
-    s.m = hi;
-  }
+  raise<DT, ENT, N>(s, w, c2);
   uint64_t R[2], Q[2];
   granule_sums<DT, ENT, false, N>(w, s.m, c2, R, Q, low);
   bool again = drop >= 0;
@@ -507,15 +602,30 @@ __device__ __forceinline__ void fold(ThreadSums& s, uint4 (&w)[N], int drop, flo
   }
 }
 
+// fold for granules that may hold places outside the row (-inf): always with
+// the clamp.
+template <int DT, bool ENT, int N>
+__device__ __forceinline__ void fold_clamped(ThreadSums& s, const uint4 (&w)[N], float c2,
+                                             unsigned& low) {
+  raise<DT, ENT, N>(s, w, c2);
+  uint64_t R[2], Q[2];
+  granule_sums<DT, ENT, true, N>(w, s.m, c2, R, Q, low);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    s.R[k] = add2(s.R[k], R[k]);
+    if (ENT) s.Q[k] = add2(s.Q[k], Q[k]);
+  }
+}
+
 // The gradient p (a0 + a1 log2 p), p = 2^((z - M) c2 - l2S), of a granule.
 template <int DT, bool ENT, bool CLAMP>
-__device__ __forceinline__ void granule_grad(const uint4& w, uint64_t nM, uint64_t c2, uint64_t nl,
+__device__ __forceinline__ void granule_grad(const uint4& w, float M, uint64_t c2, uint64_t nl,
                                              uint64_t A0, uint64_t A1,
                                              float (&o)[ScoreType<DT>::kPer16]) {
-  const Granule<DT> z = granule<DT>(w);
+  const Granule<DT> z = granule_minus<DT>(w, M);
 #pragma unroll
   for (int k = 0; k < Granule<DT>::kPairs; ++k) {
-    uint64_t x = fma2(add2(z.v[k], nM), c2, nl);
+    uint64_t x = fma2(z.v[k], c2, nl);
     float xa, xb;
     unpack2(x, xa, xb);
     if (ENT && CLAMP) {
@@ -584,22 +694,16 @@ __device__ __forceinline__ RowShare row_share(const void* buf, int64_t ld, int r
   return s;
 }
 
-template <int NW>
-struct RingShape {
-  static constexpr int kThreads = (NW + 2) * 32;
-  static constexpr int kCtas = NW == 8 ? 2 : 4;  // per SM
-};
 
-template <int DT, bool ENT, bool GRAD, int NW>
-__global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
+template <int DT, bool ENT, bool GRAD>
+__global__ void __launch_bounds__(kRingThreads, kRingCtas)
     score_ring_kernel(const ScoreArgs p, const RingArgs q) {
+  constexpr int NW = kRingWarps;
   constexpr int kB = ScoreType<DT>::kBytes, kPer = ScoreType<DT>::kPer16;
   constexpr int kT = NW * 32;
   constexpr int kIter = kStageIter;
-  constexpr int kStageGran = kT * kIter;
-  constexpr int kStageBytes = stage_bytes(NW);
-  extern __shared__ __align__(128) unsigned char ring[];
-  const RingLayout lay = ring_layout(q.stages, NW);
+    extern __shared__ __align__(128) unsigned char ring[];
+  const RingLayout lay = ring_layout(q.stages);
   float4* part = reinterpret_cast<float4*>(ring + lay.part);  // [kSlots][C NW]
   RowGrad* grad = reinterpret_cast<RowGrad*>(ring + lay.grad);  // [kSlots], 32 bytes apart
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + lay.bars);
@@ -627,15 +731,8 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
   __syncthreads();
   cluster_sync_all();
 
-  int row_lo = 0, row_hi = p.rows;
-  if (p.offsets) {
-    row_lo = p.offsets[0];
-    row_hi = p.offsets[p.n_off];
-  }
+  const RowRange range = row_range(p);
   auto row_of = [&](int i) { return q.reverse ? p.rows - 1 - i : i; };
-  auto live = [&](int row, int token, float weight) {
-    return token >= 0 && weight != 0.f && row >= row_lo && row < row_hi;
-  };
   auto fail = [&]() {
     atomicOr(p.status, kScoreTimeout);
     *(volatile int*)abort_flag = 1;
@@ -648,61 +745,56 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
   };
   bool ok = true;
   const float nan = __int_as_float(0x7fc00000);
+  double t[kPolicyTerms] = {};  // the finisher's
 
   if (warp == NW) {
     // ------------------------------------------------------------ producer
     const uint64_t once = evict_first_policy(), again = evict_last_policy();
-    int issued = 0, slot = 0;
-    uint32_t phase = 1;  // the parity of an empty stage's first wait: passes at once
-    auto copy_share = [&](int row, uint64_t policy) {
-      const RowShare s = row_share<DT>(p.logits, p.ld, row, p.V, q.log2C, rank);
-      const char* img = static_cast<const char*>(p.logits) + s.base;
-      for (int g = s.g0; g < s.g0 + s.n; g += kStageGran) {
-        if (!wait(&empty[slot], phase)) {
-          ok = false;
-          break;
-        }
-        unsigned char* dst = ring + (size_t)slot * kStageBytes;
-        const int end = min(g + kStageGran, s.g0 + s.n);
-        const int b0 = max(g, s.whole0), b1 = max(b0, min(end, s.whole1));
-        if (b0 != g || b1 != end) {
-          // granules the row fills in part: at most the first and the last
-          for (int e = lane; e < 2 * kPer; e += 32) {
-            const int gr = e < kPer ? 0 : s.whole1;
-            const bool mine = gr >= g && gr < end && (gr < b0 || gr >= b1) &&
-                              (e < kPer || s.whole1 != 0 || s.whole0 == 0);
-            const int at = gr * kPer + (e & (kPer - 1));  // element of the image
-            if (mine) {
-              const int v = at - s.shift;
-              const bool in = v >= 0 && v < p.V;
-              unsigned char* to = dst + (size_t)(gr - g) * 16 + (e & (kPer - 1)) * kB;
-              if (kB == 4)
-                *reinterpret_cast<uint32_t*>(to) =
-                    in ? reinterpret_cast<const uint32_t*>(img)[at] : 0xff800000u;
-              else
-                *reinterpret_cast<uint16_t*>(to) =
-                    in ? reinterpret_cast<const uint16_t*>(img)[at] : (uint16_t)0xff80u;
-            }
+    RingWalk walk{0, 1, q.stages, 0xffffffffu};  // an empty stage's first wait passes at once
+    uint32_t fills = 0u;  // parity of each slot's copies
+    // One stage of a share, granules g .. end - 1, into the walk's slot.
+    auto copy_stage = [&](const RowShare& s, const char* img, int g, int end, uint64_t policy) {
+      if (!wait(&empty[walk.slot], walk.phase())) {
+        ok = false;
+        return;
+      }
+      unsigned char* dst = ring + (size_t)walk.slot * kStageBytes;
+      const int b0 = max(g, s.whole0), b1 = max(b0, min(end, s.whole1));
+      if (b0 != g || b1 != end) {
+        // granules the row fills in part: at most the first and the last
+        for (int e = lane; e < 2 * kPer; e += 32) {
+          const int gr = e < kPer ? 0 : s.whole1;
+          const bool mine = gr >= g && gr < end && (gr < b0 || gr >= b1) &&
+                            (e < kPer || s.whole1 != 0 || s.whole0 == 0);
+          const int at = gr * kPer + (e & (kPer - 1));  // element of the image
+          if (mine) {
+            const int v = at - s.shift;
+            const bool in = v >= 0 && v < p.V;
+            unsigned char* to = dst + (size_t)(gr - g) * 16 + (e & (kPer - 1)) * kB;
+            if (kB == 4)
+              *reinterpret_cast<uint32_t*>(to) =
+                  in ? reinterpret_cast<const uint32_t*>(img)[at] : 0xff800000u;
+            else
+              *reinterpret_cast<uint16_t*>(to) =
+                  in ? reinterpret_cast<const uint16_t*>(img)[at] : (uint16_t)0xff80u;
           }
-          __syncwarp();
-        }
-        if (lane == 0) {
-          const uint32_t bytes = (uint32_t)(b1 - b0) * 16u;
-          mbar_arrive_expect_tx(&full[slot], bytes);
-          if (bytes)
-            bulk_load(dst + (size_t)(b0 - g) * 16, img + (size_t)b0 * 16, bytes, &full[slot],
-                      policy);
         }
         __syncwarp();
-        ++issued;
-        if (++slot == q.stages) {
-          slot = 0;
-          phase ^= 1u;
-        }
       }
+      if (lane == 0) {
+        const uint32_t bytes = (uint32_t)(b1 - b0) * 16u;
+        mbar_arrive_expect_tx(&full[walk.slot], bytes);
+        if (bytes)
+          bulk_load(dst + (size_t)(b0 - g) * 16, img + (size_t)b0 * 16, bytes, &full[walk.slot],
+                    policy);
+      }
+      __syncwarp();
+      fills ^= 1u << walk.slot;
+      walk.used();
+      walk.step();
     };
     int i = cid;
-    int token = -1, before = -1;  // before: a row still to be copied again
+    int token = -1;
     float weight = 1.f;
     if (i < p.rows) {
       token = p.tokens[row_of(i)];
@@ -710,30 +802,35 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
     }
     for (; i < p.rows && ok; i += ncl) {
       const int row = row_of(i);
-      const bool on = live(row, token, weight);
+      const bool on = range.live(row, token, weight);
       if (i + ncl < p.rows) {
         token = p.tokens[row_of(i + ncl)];
         if (p.weights) weight = p.weights[row_of(i + ncl)];
       }
       if (!on) continue;
-      const bool twice = GRAD && !q.resident;
-      copy_share(row, twice ? again : once);
-      if (twice) {
-        if (!q.ahead) before = row;
-        if (before >= 0 && ok) copy_share(before, once);
-        before = q.ahead ? row : -1;
+      const RowShare s = row_share<DT>(p.logits, p.ld, row, p.V, q.log2C, rank);
+      const char* img = static_cast<const char*>(p.logits) + s.base;
+      const int n_st = (s.n + kStageGran - 1) / kStageGran;
+      const bool back = GRAD && !q.ahead;
+      const int kept = min(n_st, q.keep);
+      for (int k = 0; k < n_st && ok; ++k)
+        copy_stage(s, img, s.g0 + k * kStageGran, s.g0 + min(s.n, (k + 1) * kStageGran),
+                   back && kept < n_st ? again : once);
+      if (back) {
+        walk.turn();
+        walk.step(kept);
+        for (int k = n_st - kept - 1; k >= 0 && ok; --k)
+          copy_stage(s, img, s.g0 + k * kStageGran, s.g0 + (k + 1) * kStageGran, once);
       }
     }
-    if (before >= 0 && ok) copy_share(before, once);
     if (!ok && lane == 0) fail();
     // every copy issued has landed before the CTA may leave
     if (lane == 0)
-      for (int k = max(0, issued - q.stages); k < issued; ++k)
-        mbar_wait(&full[k % q.stages], (uint32_t)(k / q.stages) & 1u, kDrainLimitNs);
+      for (int k = 0; k < q.stages; ++k)
+        mbar_wait(&full[k], (fills >> k & 1u) ^ 1u, kDrainLimitNs);
     __syncwarp();
   } else if (warp == NW + 1) {
     // ------------------------------------------------------------ finisher
-    double t[kPolicyTerms] = {};
     uint32_t count = 0;  // rows finished
     const bool first = rank == 0;
     if (GRAD || first) {
@@ -761,7 +858,7 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
         const float wt = weight, y0 = x0, y1 = x1, y2 = x2;
         const float Trow = row_temp_ok(T) ? T : nan;
         if (i + ncl < p.rows) fetch(row_of(i + ncl));
-        if (!live(row, a, wt)) {
+        if (!range.live(row, a, wt)) {
           if (first && lane == 0) {
             if (p.logprobs) p.logprobs[row] = 0.f;
             if (p.entropies) p.entropies[row] = 0.f;
@@ -814,15 +911,7 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
           c = policy_row(p, r, wt, y0, y1, y2, first && lane == 0, t);
         if (GRAD) {
           if (lane == 0) {
-            const float iT = 1.f / Trow;
-            RowGrad o;
-            o.M = r.M;
-            o.l2S = r.l2S;
-            o.a0 = -iT * (ENT ? fmaf(c.h, r.H, c.g) : c.g);
-            o.a1 = -iT * c.h * kLn2;
-            // p_a = 0: log p_a may be -inf, its entropy term is 0
-            const float ha = !ENT ? 0.f : r.pa > 0.f ? c.h * r.pa * (r.lp + r.H) : r.pa;
-            o.own = iT * (c.g * r.rest - ha);
+            const RowGrad o = row_grad<ENT>(r, c, Trow);
             *reinterpret_cast<RowGrad*>(reinterpret_cast<char*>(grad) + par * 32) = o;
             mbar_arrive(&result[par]);
           }
@@ -838,17 +927,10 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
       }
       if (!ok && lane == 0) fail();
     }
-    if (q.mode == kModePolicy && first && lane == 0) {
-      const bool cut = !ok || *(volatile int*)abort_flag;
-      for (int k = 0; k < kPolicyTerms; ++k)
-        p.part[(size_t)cid * kPolicyTerms + k] = cut ? (double)nan : t[k];
-    }
-    __syncwarp();
   } else {
     // ----------------------------------------------------------- consumers
-    int slot = 0;        // the next stage of the ring's order
-    uint32_t phase = 0;
-    int held = 0;        // resident: the first stage still held
+    RingWalk walk{0, 1, q.stages, 0u};
+    int held = 0;        // ahead: the first slot still held
     uint32_t count = 0;  // rows folded
     // A folded row whose gradient is still to be written.
     struct Pending {
@@ -883,17 +965,23 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
       int el;
       const int mine = place(sh, w.token, el);
       const float c2 = w.c2;
-      const uint64_t nM = pack2(-r.M, -r.M), cc = pack2(c2, c2), nl = pack2(-r.l2S, -r.l2S),
-                     A0 = pack2(r.a0, r.a0), A1 = pack2(r.a1, r.a1);
+      const uint64_t cc = pack2(c2, c2), nl = pack2(-r.l2S, -r.l2S), A0 = pack2(r.a0, r.a0), A1 = pack2(r.a1, r.a1);
       const bool deep = w.deep || (ENT && (w.m - r.M) * c2 < -kDeep);
-      int n = sh.n, first = 0, g = sh.g0 + tid;
-      while (n > 0) {
-        if (!q.resident && !wait(&full[slot], phase)) {
-          ok = false;
-          return;
+      const int n_st = (sh.n + kStageGran - 1) / kStageGran;
+      if (!q.ahead) walk.turn();
+      for (int i = 0; i < n_st; ++i) {
+        const int st_no = q.ahead ? i : n_st - 1 - i;  // the stage of the share
+        if (!q.ahead && i >= q.keep) {
+          if (!wait(&full[walk.slot], walk.phase())) {
+            ok = false;
+            return;
+          }
+          walk.used();
         }
-        const int at = q.resident ? held : slot;
+        const int at = q.ahead ? held : walk.slot;
         const uint4* st = reinterpret_cast<const uint4*>(ring + (size_t)at * kStageBytes) + tid;
+        const int n = sh.n - st_no * kStageGran, first = st_no * kIter;
+        const int g = sh.g0 + st_no * kStageGran + tid;
         // a stage of whole granules without the token, nothing to clamp
         const bool plain = (kIter - 1) * kT + tid < n && dz_vec && !deep &&
                            (unsigned)(mine - first) >= (unsigned)kIter && g >= sh.whole0 &&
@@ -903,7 +991,7 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
 #pragma unroll
           for (int j = 0; j < kIter; ++j) {
             float o[kPer];
-            granule_grad<DT, ENT, false>(st[j * kT], nM, cc, nl, A0, A1, o);
+            granule_grad<DT, ENT, false>(st[j * kT], r.M, cc, nl, A0, A1, o);
             store_stream(out + j * kT, granule_pack<DT>(o));
           }
         } else {
@@ -911,7 +999,7 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
           for (int j = 0; j < kIter && j * kT + tid < n; ++j) {
             const int gj = g + j * kT;
             float o[kPer];
-            granule_grad<DT, ENT, true>(st[j * kT], nM, cc, nl, A0, A1, o);
+            granule_grad<DT, ENT, true>(st[j * kT], r.M, cc, nl, A0, A1, o);
             if (first + j == mine) {
 #pragma unroll
               for (int k = 0; k < kPer; ++k)
@@ -930,16 +1018,10 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[at]);
-        first += kIter;
-        g += kIter * kT;
-        n -= kStageGran;
-        const int next = at + 1 == q.stages ? 0 : at + 1;
-        if (q.resident) {
-          held = next;
-        } else {
-          slot = next;
-          if (next == 0) phase ^= 1u;
-        }
+        if (q.ahead)
+          held = held + 1 == q.stages ? 0 : held + 1;
+        else
+          walk.step();
       }
     };
 
@@ -962,7 +1044,7 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
         if (p.temps) T = p.temps[row_of(i + ncl)];
       }
       const RowShare sh = row_share<DT>(p.logits, p.ld, row, p.V, q.log2C, rank);
-      if (!live(row, a, wt)) {
+      if (!range.live(row, a, wt)) {
         if (GRAD) {
           char* dz = grad_image(row, sh);
           const bool dz_vec = ((uintptr_t)dz & 15u) == 0;
@@ -989,14 +1071,18 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
       s.R[0] = s.R[1] = s.Q[0] = s.Q[1] = 0ull;
       bool deep = false;
       float za = 0.f;
-      int n = sh.n;   // granules left
-      int first = 0;  // the stage's first granule of this thread
-      while (n > 0) {
-        if (!wait(&full[slot], phase)) {
+      const int n_st = (sh.n + kStageGran - 1) / kStageGran;
+      // stages that stay for the gradient: all (ahead), or the last ones
+      const int stay = !GRAD ? 0 : q.ahead ? n_st : min(n_st, q.keep);
+      for (int k = 0; k < n_st; ++k) {
+        if (!wait(&full[walk.slot], walk.phase())) {
           ok = false;
           break;
         }
-        const uint4* st = reinterpret_cast<const uint4*>(ring + (size_t)slot * kStageBytes) + tid;
+        walk.used();
+        const uint4* st =
+            reinterpret_cast<const uint4*>(ring + (size_t)walk.slot * kStageBytes) + tid;
+        const int n = sh.n - k * kStageGran, first = k * kIter;
         const int drop =
             (unsigned)(mine - first) < (unsigned)kIter ? (mine - first) * kPer + el : -1;
         unsigned low = 0u;
@@ -1027,16 +1113,11 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
                 g + j * kT < sh.whole1)
               deep = true;
         }
-        if (!GRAD || !q.resident) {
+        if (k < n_st - stay) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[slot]);
+          if (lane == 0) mbar_arrive(&empty[walk.slot]);
         }
-        first += kIter;
-        n -= kStageGran;
-        if (++slot == q.stages) {
-          slot = 0;
-          phase ^= 1u;
-        }
+        walk.step();
       }
       if (!ok) break;
       // this warp's sums to the finishing CTAs, with the token's logit where
@@ -1080,7 +1161,181 @@ __global__ void __launch_bounds__(RingShape<NW>::kThreads, RingShape<NW>::kCtas)
   }
   __syncthreads();
   cluster_sync_all();
-  if (q.mode == kModePolicy && rank == 0) policy_total<NW + 2>(p, ncl);
+  if (q.mode == kModePolicy && rank == 0) {
+    // a cut-short pass gives NaN, not a part of the sums
+    if (*(volatile int*)abort_flag)
+      for (int k = 0; k < kPolicyTerms; ++k) t[k] = (double)nan;
+    policy_total<kRingThreads, 1>(p, tid == (NW + 1) * 32 ? 0 : -1, t, cid, ncl);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Short rows: held in registers
+//
+// W warps take a row, each lane up to 8 of its granules, and keep it from the
+// one read to the gradient's write.  A short row's cost is its latency (load,
+// sums, logarithms, store), so what counts is how many are in flight: W = 1
+// up to 4 KB, W = 4 up to 16 KB, four warps to a block, six to eight blocks to
+// an SM.
+// ---------------------------------------------------------------------------
+constexpr int kShortThreads = 128;
+constexpr int kShortGran = 8;  // granules per lane
+constexpr int kShortChunk = 2;
+constexpr __host__ __device__ int short_bytes(int W) { return W * 32 * kShortGran * 16; }
+
+template <int DT, bool ENT, bool GRAD, int W>
+__global__ void __launch_bounds__(kShortThreads, GRAD ? 6 : 8)
+    score_short_kernel(const ScoreArgs p, const int mode, const int reverse) {
+  constexpr int kB = ScoreType<DT>::kBytes, kPer = ScoreType<DT>::kPer16;
+  constexpr int kRows = kShortThreads / 32 / W;  // per block
+  constexpr int kT = W * 32;
+  __shared__ float4 warp_part[2][4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x % kT;  // in the row
+  const RowRange range = row_range(p);
+  const float nan = __int_as_float(0x7fc00000);
+  double t[kPolicyTerms] = {};
+  int flip = 0;
+  // W = 4: the block's warps share a row and meet at barriers
+  for (int i = blockIdx.x * kRows + warp / W; i < p.rows; i += gridDim.x * kRows) {
+    const int row = reverse ? p.rows - 1 - i : i;
+    const int token = p.tokens[row];
+    const float weight = p.weights ? p.weights[row] : 1.f;
+    const RowShare sh = row_share<DT>(p.logits, p.ld, row, p.V, 0, 0);
+    char* dz = nullptr;
+    bool dz_vec = false;
+    if (GRAD) {
+      dz = static_cast<char*>(p.d_logits) + (int64_t)row * p.ldd * kB - sh.shift * kB;
+      dz_vec = ((uintptr_t)dz & 15u) == 0;
+    }
+    // one granule of the gradient
+    auto put = [&](int g, const float (&o)[kPer]) {
+      if (dz_vec && g >= sh.whole0 && g < sh.whole1) {
+        store_stream(reinterpret_cast<uint4*>(dz) + g, granule_pack<DT>(o));
+      } else {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const int v = g * kPer + k - sh.shift;
+          if (v >= 0 && v < p.V) store_grad<DT>(dz, (int64_t)g * kPer + k, o[k]);
+        }
+      }
+    };
+    if (!range.live(row, token, weight)) {
+      if (tid == 0) {
+        if (p.logprobs) p.logprobs[row] = 0.f;
+        if (p.entropies) p.entropies[row] = 0.f;
+      }
+      if (GRAD) {
+        const float zero[kPer] = {};
+        for (int g = tid; g < sh.n; g += kT) put(g, zero);
+      }
+      continue;
+    }
+    // the row, in registers
+    const char* img = static_cast<const char*>(p.logits) + sh.base;
+    uint4 w[kShortGran / kShortChunk][kShortChunk];
+#pragma unroll
+    for (int c = 0; c < kShortGran; ++c) {
+      const int g = c * kT + tid;
+      uint4 x = kB == 4 ? make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u)
+                        : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+      if (g < sh.n) {
+        if (g >= sh.whole0 && g < sh.whole1) {
+          x = reinterpret_cast<const uint4*>(img)[g];
+        } else {
+          uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            const int v = g * kPer + k - sh.shift;
+            if (v < 0 || v >= p.V) continue;
+            if (kB == 4)
+              e[k & 3] = reinterpret_cast<const uint32_t*>(img)[g * 4 + (k & 3)];
+            else {
+              const uint32_t h = reinterpret_cast<const uint16_t*>(img)[g * 8 + k];
+              e[(k >> 1) & 3] = (k & 1) ? (e[(k >> 1) & 3] & 0xffffu) | h << 16
+                                        : (e[(k >> 1) & 3] & 0xffff0000u) | h;
+            }
+          }
+          x = make_uint4(e[0], e[1], e[2], e[3]);
+        }
+      }
+      w[c / kShortChunk][c % kShortChunk] = x;
+    }
+    float T = p.temps ? p.temps[row] : p.temp;
+    if (!row_temp_ok(T)) T = nan;
+    float x0 = 0.f, x1 = 0.f, x2 = 0.f;
+    if (mode == kModePolicy) {
+      x0 = p.old_lp[row];
+      x1 = p.adv[row];
+      if (p.ref_lp) x2 = p.ref_lp[row];
+    } else if (mode == kModeGrad) {
+      x0 = p.g_lp[row];
+      if (p.g_h) x1 = p.g_h[row];
+    }
+    const float c2 = kLog2e / T;
+    const bool bad = token >= p.V;
+    const int at = token + sh.shift, ag = at / kPer, el = at & (kPer - 1);
+    const int mine = !bad && ag % kT == tid ? ag / kT : -1;
+    ThreadSums s;
+    s.m = -FLT_MAX;
+    s.R[0] = s.R[1] = s.Q[0] = s.Q[1] = 0ull;
+    float za = 0.f;
+#pragma unroll
+    for (int c = 0; c < kShortGran / kShortChunk; ++c) {
+      if (c * kShortChunk * kT >= sh.n) break;  // the same in every lane
+      uint4 v[kShortChunk];
+#pragma unroll
+      for (int k = 0; k < kShortChunk; ++k) v[k] = w[c][k];
+      const int j = mine - c * kShortChunk;
+      if (j >= 0 && j < kShortChunk) za = granule_drop<DT, kShortChunk>(v, j * kPer + el);
+      unsigned low = 0u;
+      fold_clamped<DT, ENT, kShortChunk>(s, v, c2, low);
+    }
+    RowSums all = warp_join(RowSums{s.m, pair_sum(s.R), ENT ? pair_sum(s.Q) : 0.f}, c2);
+    const unsigned holder = __ballot_sync(0xffffffffu, mine >= 0);
+    za = holder ? __shfl_sync(0xffffffffu, za, __ffs(holder) - 1) : 0.f;
+    if (W > 1) {
+      if (lane == 0) warp_part[flip][warp] = make_float4(all.m, all.R, all.Q, za);
+      __syncthreads();
+      all = row_sums_empty();
+      za = 0.f;
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        const float4 v = warp_part[flip][k];
+        all = row_sums_join(all, RowSums{v.x, v.y, v.z}, c2);
+        za += v.w;
+      }
+      flip ^= 1;  // the next row's sums do not meet a slow reader of these
+    }
+    const RowResult r = row_result(all, bad ? nan : za, c2);
+    RowCoef c{x0, x1};
+    if (mode == kModePolicy) c = policy_row(p, r, weight, x0, x1, x2, tid == 0, t);
+    if (tid == 0) {
+      if (p.logprobs) p.logprobs[row] = r.lp;
+      if (ENT && p.entropies) p.entropies[row] = r.H;
+      const uint32_t bits = (bad ? kScoreBadToken : 0u) | (r.finite ? 0u : kScoreNonFinite);
+      if (bits) atomicOr(p.status, bits);
+    }
+    if (GRAD) {
+      const RowGrad f = row_grad<ENT>(r, c, T);
+      const uint64_t cc = pack2(c2, c2), nl = pack2(-f.l2S, -f.l2S), A0 = pack2(f.a0, f.a0), A1 = pack2(f.a1, f.a1);
+#pragma unroll
+      for (int c1 = 0; c1 < kShortGran; ++c1) {
+        const int g = c1 * kT + tid;
+        if (g >= sh.n) break;
+        float o[kPer];
+        granule_grad<DT, ENT, true>(w[c1 / kShortChunk][c1 % kShortChunk], f.M, cc, nl, A0, A1, o);
+        if (c1 == mine) {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k)
+            if (k == el) o[k] = f.own;
+        }
+        put(g, o);
+      }
+    }
+  }
+  if (mode == kModePolicy)
+    policy_total<kShortThreads, kRows>(p, tid == 0 ? warp / W : -1, t, blockIdx.x, gridDim.x);
 }
 
 // ---------------------------------------------------------------------------
