@@ -151,7 +151,7 @@ __device__ __forceinline__ RowResult row_result(RowSums s, float za, float c2) {
   const float S = R + ea;
   float lnS;
   if (ea >= R) {
-    const float t = log1pf(R / ea);
+    const float t = log1pf(__fdividef(R, ea));
     lnS = fmaf(da, kLn2, t);
     r.lp = -t;
   } else {
@@ -162,9 +162,10 @@ __device__ __forceinline__ RowResult row_result(RowSums s, float za, float c2) {
   r.l2S = lnS * kLog2e;
   // e_a = 0: no entropy term, whatever d_a
   const float W = ea == 0.f ? Q : fmaf(ea, da, Q);
-  r.H = fmaf(-kLn2, W / S, lnS);
+  const float iS = __frcp_rn(S);
+  r.H = fmaf(-kLn2, W * iS, lnS);
   r.rest = R / S;
-  r.pa = ea / S;
+  r.pa = ea * iS;
   r.finite = S > 0.f && S < INFINITY;
   if (!r.finite) r.lp = r.H = r.l2S = r.rest = r.pa = __int_as_float(0x7fc00000);
   return r;
@@ -210,38 +211,51 @@ __device__ __forceinline__ RowRange row_range(const ScoreArgs& p) {
   return r;
 }
 
-// The policy loss of a row: its gradients, and its terms added to t.
+// The policy loss of a row.
 //   L = w [ max(-A r, -A clip(r)) + k KL - c H ],  r = exp(log p_a - old),
 //   KL = exp(ref - log p_a) - 1 - (ref - log p_a)
-__device__ __forceinline__ RowCoef policy_row(const ScoreArgs& p, const RowResult& r, float weight,
-                                              float old_lp, float adv, float ref_lp, bool count,
-                                              double (&t)[kPolicyTerms]) {
+struct PolicyRow {
+  float pg, kl, dkl;
+  bool cut;  // the clipped side is the larger: no gradient through the ratio
+};
+
+__device__ __forceinline__ PolicyRow policy_row(const ScoreArgs& p, const RowResult& r,
+                                                float old_lp, float adv, float ref_lp) {
   const float ratio = expf(r.lp - old_lp);
   const float free = -adv * ratio;
   // the comparisons keep a NaN ratio NaN
   const float held_ratio = ratio < p.clip_lo ? p.clip_lo : ratio > p.clip_hi ? p.clip_hi : ratio;
   const float held = -adv * held_ratio;
-  const bool cut = held > free;
-  float kl = 0.f, dkl = 0.f;
+  PolicyRow o;
+  o.cut = held > free;
+  o.pg = o.cut ? held : free;
+  o.kl = o.dkl = 0.f;
   if (p.ref_lp) {
     const float gap = ref_lp - r.lp;
     const float back = expm1f(gap);
-    kl = back - gap;
-    dkl = -back;
+    o.kl = back - gap;
+    o.dkl = -back;
   }
-  if (count) {
-    const double w = (double)weight * p.scale, pg = cut ? held : free;
-    t[0] += w * (pg + (double)p.kl_coef * kl - (double)p.ent_coef * r.H);
-    t[1] += w * pg;
-    t[2] += w * kl;
-    t[3] += w * r.H;
-    t[4] += cut ? w : 0.0;
-  }
+  return o;
+}
+
+__device__ __forceinline__ RowCoef policy_coef(const ScoreArgs& p, const PolicyRow& o,
+                                               float weight) {
   const float w = weight * (float)p.scale;
   RowCoef c;
-  c.g = w * fmaf(p.kl_coef, dkl, cut ? 0.f : free);
+  c.g = w * fmaf(p.kl_coef, o.dkl, o.cut ? 0.f : o.pg);
   c.h = -w * p.ent_coef;
   return c;
+}
+
+__device__ __forceinline__ void policy_add(const ScoreArgs& p, const PolicyRow& o, float H,
+                                           float weight, double (&t)[kPolicyTerms]) {
+  const double w = (double)weight * p.scale;
+  t[0] += w * ((double)o.pg + (double)p.kl_coef * o.kl - (double)p.ent_coef * H);
+  t[1] += w * o.pg;
+  t[2] += w * o.kl;
+  t[3] += w * H;
+  t[4] += o.cut ? w : 0.0;
 }
 
 // The loss's terms.  A CTA's part is the sum of its leaders' t (one thread
@@ -907,12 +921,15 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
         const bool bad = a >= p.V;
         const RowResult r = row_result(all, bad ? nan : za, c2);
         RowCoef c{y0, y1};
-        if (q.mode == kModePolicy)
-          c = policy_row(p, r, wt, y0, y1, y2, first && lane == 0, t);
+        PolicyRow o{};
+        if (q.mode == kModePolicy) {
+          o = policy_row(p, r, y0, y1, y2);
+          c = policy_coef(p, o, wt);
+        }
         if (GRAD) {
           if (lane == 0) {
-            const RowGrad o = row_grad<ENT>(r, c, Trow);
-            *reinterpret_cast<RowGrad*>(reinterpret_cast<char*>(grad) + par * 32) = o;
+            const RowGrad f = row_grad<ENT>(r, c, Trow);
+            *reinterpret_cast<RowGrad*>(reinterpret_cast<char*>(grad) + par * 32) = f;
             mbar_arrive(&result[par]);
           }
           __syncwarp();
@@ -922,6 +939,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
           if (ENT && p.entropies) p.entropies[row] = r.H;
           const uint32_t bits = (bad ? kScoreBadToken : 0u) | (r.finite ? 0u : kScoreNonFinite);
           if (bits) atomicOr(p.status, bits);
+          if (q.mode == kModePolicy) policy_add(p, o, r.H, wt, t);
         }
         ++count;
       }
@@ -1309,7 +1327,11 @@ __global__ void __launch_bounds__(kShortThreads, GRAD ? 6 : 8)
     }
     const RowResult r = row_result(all, bad ? nan : za, c2);
     RowCoef c{x0, x1};
-    if (mode == kModePolicy) c = policy_row(p, r, weight, x0, x1, x2, tid == 0, t);
+    if (mode == kModePolicy) {
+      const PolicyRow o = policy_row(p, r, x0, x1, x2);
+      c = policy_coef(p, o, weight);
+      if (tid == 0) policy_add(p, o, r.H, weight, t);
+    }
     if (tid == 0) {
       if (p.logprobs) p.logprobs[row] = r.lp;
       if (ENT && p.entropies) p.entropies[row] = r.H;
