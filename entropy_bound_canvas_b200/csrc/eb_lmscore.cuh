@@ -3,12 +3,25 @@
 // tile on the tensor cores and reduced on chip, so the logits never reach
 // HBM.
 //
-// A CTA owns one 128-row tile and a contiguous range of the 256-wide
-// vocabulary tiles.  Warp 0 loads (TMA), warp 1 issues tcgen05.mma into one
-// of two TMEM accumulators, warps 2-5 hold one row per thread and fold each
-// accumulator into the row's sums (row_sums of eb_score.cuh).  Columns past V
-// and hidden elements past d read as zeros and the columns are left out.  The
-// ranges' sums are joined in vocabulary order by lmscore_finish_kernel.
+// A pair of CTAs (a cluster of two, one per SM) owns 256 rows and a contiguous
+// range of the 256-wide vocabulary tiles; each CTA loads its own 128 rows of h
+// and half of each W tile, and one tcgen05.mma.cta_group::2 works on both
+// SMs' shared memory, so a W tile crosses the L2 once per pair.  Roles:
+//   warp 0     loads (TMA, 128-byte swizzle) into a ring of 32 KB stages; both
+//              CTAs' copies are counted by the first CTA's barriers;
+//   warp 1     of the first CTA issues the MMAs (M = 256, N = 256, K = 16) into
+//              one of two accumulators (2 x 256 TMEM columns in each CTA);
+//   warps 2-9  read the accumulators: a thread holds one row and 128 columns.
+//
+// The tensor cores add each K = 16 step's products to the accumulator with
+// truncation: about 2^-26 of the sum lost per step, always toward zero (1.6e-8
+// measured; over the 160 steps of d = 2560 a logit of 10 was 2.6e-5 low, five
+// times what fp32 summation loses).  So an accumulator takes 512 elements of K
+// at most, and the pieces are added in registers, rounded to nearest.
+//
+// Columns past V and hidden elements past d read as zeros; the columns are
+// left out of the sums.  The ranges' sums are joined in vocabulary order by
+// lmscore_finish_kernel.
 #pragma once
 
 #include "eb_score.cuh"
@@ -16,10 +29,16 @@
 
 namespace ebk {
 
-constexpr int kLsBM = 128, kLsBN = 256, kLsBK = 64;
-constexpr int kLsStages = 4;
-constexpr int kLsThreads = 6 * 32;
-constexpr uint32_t kLsABytes = kLsBM * kLsBK * 2, kLsBBytes = kLsBN * kLsBK * 2;
+constexpr int kLsRows = 128;          // rows per CTA
+constexpr int kLsBM = 2 * kLsRows;    // rows per pair
+constexpr int kLsBN = 256, kLsBK = 64;
+constexpr int kLsHalf = kLsBN / 2;    // rows of W a CTA loads, columns a thread holds
+constexpr int kLsStages = 6;
+constexpr int kLsChunk = 8;           // stages of one accumulator: 512 elements of K
+constexpr int kLsEpiWarps = 8;
+constexpr int kLsThreads = (2 + kLsEpiWarps) * 32;
+constexpr uint32_t kLsABytes = kLsRows * kLsBK * 2, kLsBBytes = kLsHalf * kLsBK * 2;
+constexpr uint32_t kLsStageBytes = kLsABytes + kLsBBytes;
 constexpr uint32_t kLsTmemCols = 2 * kLsBN;
 
 using LmSums = RowSums;
@@ -28,7 +47,7 @@ struct LmScoreArgs {
   const int32_t* tokens;
   const float* temps;
   float temp;
-  LmSums* sums;  // [n_split][rows]
+  LmSums* sums;  // [2 n_split][rows]
   float* za;     // [rows] the tokens' logits
   int rows, V, d, n_split;
   uint64_t wait_ns;
@@ -37,29 +56,74 @@ struct LmScoreArgs {
   float* entropies;
 };
 
-// Vocabulary ranges per row tile: one CTA per SM over all tiles.
+// Vocabulary ranges per row tile: one pair per two SMs over all tiles.
 inline int lm_score_split(int sms, int64_t rows, int64_t V) {
   const int64_t n_mt = (rows + kLsBM - 1) / kLsBM, n_nt = (V + kLsBN - 1) / kLsBN;
-  const int64_t s = n_nt < sms / n_mt ? n_nt : sms / n_mt;
+  const int64_t fit = sms / 2 / n_mt;
+  const int64_t s = n_nt < fit ? n_nt : fit;
   return s < 1 ? 1 : (int)s;
 }
 
-// Most (range, row) records of any call of up to max_rows rows.
+// Most (half range, row) records of any call of up to max_rows rows.
 inline size_t lm_score_slots(int sms, int64_t max_rows) {
-  const size_t wide = (size_t)sms * (size_t)kLsBM;
-  return (size_t)max_rows > wide ? (size_t)max_rows : wide;
+  const size_t wide = (size_t)sms * (size_t)kLsBM, tall = 2 * (size_t)max_rows;
+  return tall > wide ? tall : wide;
 }
 
 struct LmScoreLayout {
-  uint32_t a, b, bars, total;
+  uint32_t bars, total;
 };
-__host__ __device__ inline LmScoreLayout lm_score_layout() {
-  LmScoreLayout y;
-  y.a = 0;
-  y.b = kLsStages * kLsABytes;
-  y.bars = y.b + kLsStages * kLsBBytes;
+__host__ __device__ constexpr LmScoreLayout lm_score_layout() {
+  LmScoreLayout y{};
+  y.bars = kLsStages * kLsStageBytes;
   y.total = y.bars + 8u * (2 * kLsStages + 5) + 16u + 1024u;
   return y;
+}
+
+// -- the cta_group::2 forms ------------------------------------------------------
+// This CTA's part of a stage, counted by the barrier at `bar` (a cluster
+// address: the pair's first CTA).  Reads this GPU's own memory.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y,
+                                              uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;"
+      :
+      : "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tc2_alloc(uint32_t* dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+               :
+               : "r"(smem_u32(dst)), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tc2_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" : : "r"(taddr), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tc2_relinquish() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+// Arrives on the barrier at this offset in both CTAs once every MMA issued so
+// far has completed.
+__device__ __forceinline__ void tc2_commit(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], m;\n\t}"
+      :
+      : "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tc2_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :
+      : "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 __device__ __forceinline__ float lm_temp(const LmScoreArgs& p, int row) {
@@ -67,16 +131,46 @@ __device__ __forceinline__ float lm_temp(const LmScoreArgs& p, int row) {
   return row_temp_ok(T) ? T : __int_as_float(0x7fc00000);
 }
 
-__global__ void __launch_bounds__(kLsThreads, 1)
+// Folds 128 columns (pairs) into a row's sums.  CLAMP: some of them were set
+// to -inf.
+template <bool CLAMP>
+__device__ __forceinline__ void lm_fold(RowSums& s, const uint64_t (&z)[kLsHalf / 2], float c2) {
+  float hi = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kLsHalf / 2; ++i) {
+    float a, b;
+    unpack2(z[i], a, b);
+    hi = fmaxf(hi, fmaxf(a, b));
+  }
+  if ((hi - s.m) * c2 > kLazy) s = row_sums_join(s, RowSums{hi, 0.f, 0.f}, c2);
+  const uint64_t nm = pack2(-s.m, -s.m), cc = pack2(c2, c2);
+  uint64_t R[2] = {}, Q[2] = {};
+#pragma unroll
+  for (int i = 0; i < kLsHalf / 2; ++i) {
+    uint64_t d = mul2(add2(z[i], nm), cc);
+    float d0, d1;
+    unpack2(d, d0, d1);
+    if (CLAMP) {
+      d0 = d0 < -kDeep ? -kDeep : d0;
+      d1 = d1 < -kDeep ? -kDeep : d1;
+      d = pack2(d0, d1);
+    }
+    const uint64_t e = pack2(ex2(d0), ex2(d1));
+    R[i & 1] = add2(R[i & 1], e);
+    Q[i & 1] = fma2(e, d, Q[i & 1]);
+  }
+  s.R += pair_sum(R);
+  s.Q += pair_sum(Q);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLsThreads, 1)
     lmscore_kernel(const __grid_constant__ CUtensorMap tm_h,
                    const __grid_constant__ CUtensorMap tm_w, const LmScoreArgs p) {
   extern __shared__ unsigned char ls_smem_raw[];
-  const LmScoreLayout lay = lm_score_layout();
+  // the same offset in both CTAs: the MMA's descriptors and the commits name it
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(ls_smem_raw) + 1023) & ~(uintptr_t)1023);
-  unsigned char* sa = smem + lay.a;
-  unsigned char* sb = smem + lay.b;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.bars);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lm_score_layout().bars);
   uint64_t* empty = full + kLsStages;
   uint64_t* acc_full = empty + kLsStages;  // [2]
   uint64_t* acc_empty = acc_full + 2;      // [2]
@@ -85,12 +179,15 @@ __global__ void __launch_bounds__(kLsThreads, 1)
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_rank();
+  const int pair = blockIdx.x >> 1;
   const int n_nt = (p.V + kLsBN - 1) / kLsBN;
-  const int mt = blockIdx.x / p.n_split, ns = blockIdx.x % p.n_split;
+  const int mt = pair / p.n_split, ns = pair % p.n_split;
   const int nt_lo = (int)((long long)ns * n_nt / p.n_split);
   const int nt_hi = (int)((long long)(ns + 1) * n_nt / p.n_split);
   const int n_tiles = nt_hi - nt_lo;
   const int KB = (p.d + kLsBK - 1) / kLsBK;
+  const int row0 = mt * kLsBM + rank * kLsRows;
 
   if (tid == 0) {
     for (int s = 0; s < kLsStages; ++s) {
@@ -99,15 +196,16 @@ __global__ void __launch_bounds__(kLsThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 4);
+      mbar_init(&acc_empty[b], 2 * kLsEpiWarps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 0) tc_alloc(tmem_slot, kLsTmemCols);
+  if (warp == 0) tc2_alloc(tmem_slot, kLsTmemCols);
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -116,153 +214,193 @@ __global__ void __launch_bounds__(kLsThreads, 1)
     *(volatile int*)abort_flag = 1;
   };
 
-  int issued = 0, consumed = 0;
   if (warp == 0) {
+    // ---------------------------------------------------------- producer
     if (lane == 0) {
-      const uint64_t keep = evict_last_policy(), once = evict_first_policy();
-      for (int t = 0; t < n_tiles && !*(volatile int*)abort_flag; ++t) {
-        for (int kb = 0; kb < KB; ++kb, ++issued) {
-          const int s = issued % kLsStages;
-          if (issued >= kLsStages && !mbar_wait(&empty[s], (uint32_t)(issued / kLsStages - 1) & 1u,
-                                                p.wait_ns, abort_flag)) {
+      const uint64_t keep = evict_last_policy();  // h: every vocabulary tile reads it again
+      // W: read once, or by every row tile at about the same time
+      const uint64_t wpol = p.rows > kLsBM ? keep : evict_first_policy();
+      int s = 0;
+      uint32_t phase = 1u;  // an empty stage's first wait passes at once
+      bool ok = true;
+      for (int t = 0; t < n_tiles && ok; ++t) {
+        const int y = (nt_lo + t) * kLsBN + rank * kLsHalf;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait(&empty[s], phase, p.wait_ns, abort_flag)) {
             fail();
+            ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[s], kLsABytes + kLsBBytes);
-          tma_load_2d(sa + s * kLsABytes, &tm_h, kb * kLsBK, mt * kLsBM, &full[s], keep);
-          tma_load_2d(sb + s * kLsBBytes, &tm_w, kb * kLsBK, (nt_lo + t) * kLsBN, &full[s], once);
+          // the first CTA's barrier counts both CTAs' bytes
+          const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kLsStageBytes);
+          unsigned char* dst = smem + s * kLsStageBytes;
+          tma_load_pair(dst, &tm_h, kb * kLsBK, row0, bar, keep);
+          tma_load_pair(dst + kLsABytes, &tm_w, kb * kLsBK, y, bar, wpol);
+          if (++s == kLsStages) {
+            s = 0;
+            phase ^= 1u;
+          }
         }
       }
-      for (int i = max(0, issued - kLsStages); i < issued; ++i)
-        mbar_wait(&full[i % kLsStages], (uint32_t)(i / kLsStages) & 1u, kDrainLimitNs);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    // ------------------------------------------------------- MMA issuer
+    if (rank == 0 && lane == 0) {
       constexpr uint32_t idesc = lm_idesc(kLsBM, kLsBN);
-      const uint32_t a0 = smem_u32(sa), b0 = smem_u32(sb);
-      for (int t = 0; t < n_tiles && !*(volatile int*)abort_flag; ++t) {
-        const int buf = t & 1;
-        if (t >= 2 && !mbar_wait(&acc_empty[buf], (uint32_t)(t / 2 - 1) & 1u, p.wait_ns,
-                                 abort_flag)) {
-          fail();
-          break;
-        }
-        tc_fence_after();
-        bool ok = true;
-        for (int kb = 0; kb < KB; ++kb, ++consumed) {
-          const int s = consumed % kLsStages;
-          if (!mbar_wait(&full[s], (uint32_t)(consumed / kLsStages) & 1u, p.wait_ns, abort_flag)) {
+      const uint32_t base = smem_u32(smem);
+      int s = 0, used = 0;  // stage; accumulators filled
+      uint32_t phase = 0u;
+      bool ok = true;
+      for (int t = 0; t < n_tiles && ok; ++t) {
+        for (int kb = 0; kb < KB && ok; ++kb) {
+          const int buf = used & 1, in_chunk = kb % kLsChunk;
+          if (in_chunk == 0 && used >= 2) {
+            if (!mbar_wait(&acc_empty[buf], (uint32_t)(used / 2 - 1) & 1u, p.wait_ns,
+                           abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
+          if (!mbar_wait(&full[s], phase, p.wait_ns, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
+          const uint32_t a = base + (uint32_t)s * kLsStageBytes, b = a + kLsABytes;
 #pragma unroll
           for (int k = 0; k < kLsBK / 16; ++k)
-            tc_mma(tmem + (uint32_t)(buf * kLsBN),
-                   sw128_desc(a0 + (uint32_t)(s * kLsABytes + k * 32)),
-                   sw128_desc(b0 + (uint32_t)(s * kLsBBytes + k * 32)), idesc,
-                   (kb | k) != 0 ? 1u : 0u);
-          tc_commit(&empty[s]);
+            tc2_mma(tmem + (uint32_t)(buf * kLsBN), sw128_desc(a + k * 32u), sw128_desc(b + k * 32u),
+                    idesc, (in_chunk | k) != 0 ? 1u : 0u);
+          tc2_commit(&empty[s]);  // in both CTAs: the stage has been read
+          if (++s == kLsStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+          if (in_chunk == kLsChunk - 1 || kb == KB - 1) {
+            tc2_commit(&acc_full[buf]);
+            ++used;
+          }
         }
-        if (!ok) {
-          fail();
-          break;
-        }
-        tc_commit(&acc_full[buf]);
       }
-      tc_commit(drain);
+      if (!ok) fail();
+      // every MMA issued has completed before TMEM is released
+      tc2_commit(drain);
       mbar_wait(drain, 0u, kDrainLimitNs);
     }
   } else {
-    const int q = warp & 3;  // TMEM lanes 32 q .. 32 q + 31
-    const int row = mt * kLsBM + 32 * q + lane;
+    // --------------------------------------------------------- epilogue
+    const int q = warp & 3;              // TMEM lanes 32 q .. 32 q + 31
+    const int half = (warp - 2) >> 2;    // columns 128 half ..
+    const int row = row0 + 32 * q + lane;
     const bool valid = row < p.rows;
     const int token = valid ? p.tokens[row] : -1;
     const float c2 = valid ? kLog2e / lm_temp(p, row) : 1.f;
+    const uint32_t free_bar[2] = {map_rank(smem_u32(&acc_empty[0]), 0),
+                                  map_rank(smem_u32(&acc_empty[1]), 0)};
+    const int chunks = (KB + kLsChunk - 1) / kLsChunk;
     RowSums s = row_sums_empty();
-    for (int t = 0; t < n_tiles; ++t) {
-      const int buf = t & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (uint32_t)(t / 2) & 1u, p.wait_ns,
-                                             abort_flag))) {
-        if (lane == 0) fail();
-        break;
-      }
-      tc_fence_after();
-      const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * kLsBN);
+    int used = 0;
+    bool ok = true;
+    for (int t = 0; t < n_tiles && ok; ++t) {
+      uint64_t z[kLsHalf / 2];
 #pragma unroll 1
-      for (int g = 0; g < kLsBN / 32; ++g) {
-        float z[32];
-        __syncwarp();  // tcgen05.ld is warp-wide: every lane, converged
-        tc_ld32(taddr + (uint32_t)(g * 32), z);
-        tc_wait_ld();
-        const int v0 = (nt_lo + t) * kLsBN + g * 32;
-        const int n = min(32, p.V - v0);
-        if (n <= 0) continue;
-        const int at = token - v0;
-        if (at >= 0 && at < n) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i == at) {
-              p.za[row] = z[i];
-              z[i] = -INFINITY;
-            }
+      for (int c = 0; c < chunks; ++c, ++used) {
+        const int buf = used & 1;
+        // a warp-uniform outcome: the TMEM loads below need the whole warp
+        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (uint32_t)(used / 2) & 1u,
+                                               p.wait_ns, abort_flag))) {
+          ok = false;
+          break;
         }
-        if (n < 32) {
+        tc_fence_after();
+        const uint32_t taddr =
+            tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * kLsBN + half * kLsHalf);
+        if (c == 0) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i >= n) z[i] = -INFINITY;
+          for (int i = 0; i < kLsHalf / 2; ++i) z[i] = 0ull;
         }
-        float m = z[0];
 #pragma unroll
-        for (int i = 1; i < 32; ++i) m = fmaxf(m, z[i]);
-        if (m > s.m) s = row_sums_join(s, RowSums{m, 0.f, 0.f}, c2);
-        float r4[4] = {}, q4[4] = {};
+        for (int g = 0; g < kLsHalf / 16; ++g) {
+          float v[16];
+          __syncwarp();  // tcgen05.ld is warp-wide: every lane, converged
+          tc_ld16(taddr + (uint32_t)(g * 16), v);
+          tc_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float d = (z[i] - s.m) * c2;
-          d = d < -kDeep ? -kDeep : d;
-          const float e = ex2(d);
-          r4[i & 3] += e;
-          q4[i & 3] = fmaf(e, d, q4[i & 3]);
+          for (int i = 0; i < 8; ++i) z[8 * g + i] = add2(z[8 * g + i], pack2(v[2 * i], v[2 * i + 1]));
         }
-        s.R += (r4[0] + r4[1]) + (r4[2] + r4[3]);
-        s.Q += (q4[0] + q4[1]) + (q4[2] + q4[3]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_remote(free_bar[buf]);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      if (!ok) break;
+      const int v0 = (nt_lo + t) * kLsBN + half * kLsHalf;
+      const int n = p.V - v0;  // columns of this half inside the vocabulary
+      const int at = token - v0;
+      const bool here = at >= 0 && at < min(n, kLsHalf);
+      if (n < kLsHalf || __any_sync(0xffffffffu, here)) {
+#pragma unroll
+        for (int i = 0; i < kLsHalf / 2; ++i) {
+          float a, b;
+          unpack2(z[i], a, b);
+          if (here && i == at >> 1) {
+            p.za[row] = at & 1 ? b : a;
+            if (at & 1)
+              b = -INFINITY;
+            else
+              a = -INFINITY;
+          }
+          z[i] = pack2(2 * i < n ? a : -INFINITY, 2 * i + 1 < n ? b : -INFINITY);
+        }
+        lm_fold<true>(s, z, c2);
+      } else {
+        lm_fold<false>(s, z, c2);
+      }
     }
-    // a cut-short pass leaves NaN, not stale sums
-    if (*(volatile int*)abort_flag) s.R = __int_as_float(0x7fc00000);
-    if (valid) p.sums[(size_t)ns * (size_t)p.rows + (size_t)row] = s;
+    if (!ok) {
+      if (lane == 0) fail();
+      s.R = __int_as_float(0x7fc00000);  // a cut-short pass leaves NaN, not a part of the sums
+    }
+    if (valid) p.sums[(size_t)(2 * ns + half) * (size_t)p.rows + (size_t)row] = s;
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
+  // after a cut-short pass copies may still be on their way into either CTA:
+  // they land well within this pause
+  if (*(volatile int*)abort_flag) __nanosleep(200000);
+  __syncwarp();
+  cluster_sync_all();
   tc_fence_after();
   if (warp == 0) {
     __syncwarp();
-    tc_dealloc(tmem, kLsTmemCols);
-    tc_relinquish();
+    tc2_dealloc(tmem, kLsTmemCols);
+    tc2_relinquish();
   }
 }
 
-// One thread per row: the ranges' sums in vocabulary order, then the row's
-// results.
-__global__ void lmscore_finish_kernel(const LmScoreArgs p) {
-  const int row = blockIdx.x * blockDim.x + threadIdx.x;
+// A warp per row: the ranges' sums, then the row's results.
+__global__ void __launch_bounds__(128) lmscore_finish_kernel(const LmScoreArgs p) {
+  const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= p.rows) return;
   const int token = p.tokens[row];
   if (token < 0) {
-    p.logprobs[row] = 0.f;
-    if (p.entropies) p.entropies[row] = 0.f;
+    if (lane == 0) {
+      p.logprobs[row] = 0.f;
+      if (p.entropies) p.entropies[row] = 0.f;
+    }
     return;
   }
-  const float c2 = kLog2e / lm_temp(p, row);
-  RowSums s = p.sums[row];
-  for (int k = 1; k < p.n_split; ++k)
-    s = row_sums_join(s, p.sums[(size_t)k * (size_t)p.rows + (size_t)row], c2);
   const bool bad = token >= p.V;
-  const RowResult r = row_result(s, bad ? __int_as_float(0x7fc00000) : p.za[row], c2);
+  const float za = bad ? __int_as_float(0x7fc00000) : p.za[row];
+  const float c2 = kLog2e / lm_temp(p, row);
+  RowSums s = row_sums_empty();
+  for (int k = lane; k < 2 * p.n_split; k += 32)
+    s = row_sums_join(s, p.sums[(size_t)k * (size_t)p.rows + (size_t)row], c2);
+  s = warp_join(s, c2);
+  const RowResult r = row_result(s, za, c2);
+  if (lane != 0) return;
   p.logprobs[row] = r.lp;
   if (p.entropies) p.entropies[row] = r.H;
   const uint32_t bits = (bad ? kScoreBadToken : 0u) | (r.finite ? 0u : kScoreNonFinite);

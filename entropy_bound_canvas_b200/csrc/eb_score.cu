@@ -504,17 +504,17 @@ int eb_lmhead_logprobs(eb_scorer_t* h, const void* hidden, const void* weight, i
   p.status = h->status;
   p.logprobs = logprobs;
   p.entropies = entropies;
-  if ((size_t)p.n_split * (size_t)rows > h->lm_slots) return EB_ERR_OVERFLOW;
+  if (2 * (size_t)p.n_split * (size_t)rows > h->lm_slots) return EB_ERR_OVERFLOW;
   CUtensorMap th, tw;
-  if (!ebk::make_tmap(&th, hidden, (uint64_t)d, (uint64_t)rows, ebk::kLsBK, ebk::kLsBM) ||
-      !ebk::make_tmap(&tw, weight, (uint64_t)d, (uint64_t)V, ebk::kLsBK, ebk::kLsBN))
+  if (!ebk::make_tmap(&th, hidden, (uint64_t)d, (uint64_t)rows, ebk::kLsBK, ebk::kLsRows) ||
+      !ebk::make_tmap(&tw, weight, (uint64_t)d, (uint64_t)V, ebk::kLsBK, ebk::kLsHalf))
     return EB_ERR_CUDA;
   const size_t smem = ebk::lm_score_layout().total;
   if (smem > h->optin) return EB_ERR_UNSUPPORTED;
   const int n_mt = (rows + ebk::kLsBM - 1) / ebk::kLsBM;
-  ebk::lmscore_kernel<<<n_mt * p.n_split, ebk::kLsThreads, smem, st>>>(th, tw, p);
+  ebk::lmscore_kernel<<<2 * n_mt * p.n_split, ebk::kLsThreads, smem, st>>>(th, tw, p);
   if (cudaGetLastError() != cudaSuccess) return EB_ERR_CUDA;
-  ebk::lmscore_finish_kernel<<<(rows + 127) / 128, 128, 0, st>>>(p);
+  ebk::lmscore_finish_kernel<<<(rows + 3) / 4, 128, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? EB_OK : EB_ERR_CUDA;
 }
 
