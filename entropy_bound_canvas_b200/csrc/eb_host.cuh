@@ -7,6 +7,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cstring>
 #include <mutex>
 
 namespace ebk {
@@ -24,6 +25,23 @@ struct DeviceGuard {
 };
 
 inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+// A kernel launched as a programmatic dependent of the previous one on `st`.
+inline bool launch_dependent(const void* fn, dim3 grid, dim3 block, size_t smem, void** args,
+                             cudaStream_t st) {
+  cudaLaunchConfig_t lc;
+  std::memset(&lc, 0, sizeof(lc));
+  lc.gridDim = grid;
+  lc.blockDim = block;
+  lc.dynamicSmemBytes = smem;
+  lc.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelExC(&lc, fn, args) == cudaSuccess;
+}
 
 inline PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;

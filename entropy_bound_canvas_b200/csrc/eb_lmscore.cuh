@@ -16,10 +16,15 @@
 // The tensor cores add each K = 16 step's products to the accumulator with
 // truncation: about 2^-26 of the sum lost per step, always toward zero (1.6e-8
 // measured; over the 160 steps of d = 2560 a logit of 10 was 2.6e-5 low, five
-// times what fp32 summation loses).  So an accumulator takes 512 elements of K
-// at most, and the pieces are added in registers, rounded to nearest.
+// times what fp32 summation loses).  So an accumulator takes 1024 elements of
+// K at most, and the pieces are added in registers, rounded to nearest (512
+// cost 6 % of the time of 2048 rows, 1024 less than 1 %).
 //
-// Columns past V and hidden elements past d read as zeros; the columns are
+// Up to 64 rows that product would be mostly padding: lmfew_kernel turns it
+// around (W's rows on the 128 TMEM lanes, h's as 32 or 64 columns), so that
+// only the reading of W is left.
+//
+// Vocabulary ids past V and hidden elements past d read as zeros; the ids are
 // left out of the sums.  The ranges' sums are joined in vocabulary order by
 // lmscore_finish_kernel.
 #pragma once
@@ -34,7 +39,7 @@ constexpr int kLsBM = 2 * kLsRows;    // rows per pair
 constexpr int kLsBN = 256, kLsBK = 64;
 constexpr int kLsHalf = kLsBN / 2;    // rows of W a CTA loads, columns a thread holds
 constexpr int kLsStages = 6;
-constexpr int kLsChunk = 8;           // stages of one accumulator: 512 elements of K
+constexpr int kLsChunk = 16;          // stages of one accumulator: 1024 elements of K
 constexpr int kLsEpiWarps = 8;
 constexpr int kLsThreads = (2 + kLsEpiWarps) * 32;
 constexpr uint32_t kLsABytes = kLsRows * kLsBK * 2, kLsBBytes = kLsHalf * kLsBK * 2;
@@ -47,9 +52,11 @@ struct LmScoreArgs {
   const int32_t* tokens;
   const float* temps;
   float temp;
-  LmSums* sums;  // [2 n_split][rows]
+  LmSums* sums;  // [n_rec][rows]
   float* za;     // [rows] the tokens' logits
-  int rows, V, d, n_split;
+  int rows, V, d;
+  int n_split;  // vocabulary ranges (per row tile)
+  int n_rec;    // records per row
   uint64_t wait_ns;
   uint32_t* status;
   float* logprobs;
@@ -64,7 +71,8 @@ inline int lm_score_split(int sms, int64_t rows, int64_t V) {
   return s < 1 ? 1 : (int)s;
 }
 
-// Most (half range, row) records of any call of up to max_rows rows.
+// Most (half range, row) records of any call of up to max_rows rows: sms / 2
+// / n_mt ranges of n_mt 256-row tiles, two halves each, or one range.
 inline size_t lm_score_slots(int sms, int64_t max_rows) {
   const size_t wide = (size_t)sms * (size_t)kLsBM, tall = 2 * (size_t)max_rows;
   return tall > wide ? tall : wide;
@@ -380,11 +388,274 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLsThreads, 1)
   }
 }
 
-// A warp per row: the ranges' sums, then the row's results.
+// ---------------------------------------------------------------------------
+// Few rows
+//
+// A CTA owns a contiguous range of 128-wide vocabulary tiles and every row:
+// W's 128 rows are the MMA's M, the hidden states its N = 32 NH.  A thread of
+// the epilogue holds one vocabulary id and 16 rows, and keeps a running
+// (reference, sum e, sum e d) for each of them over all its tiles; lanes and
+// warps meet once, at the end.
+// ---------------------------------------------------------------------------
+constexpr int kLfRows = 64;
+constexpr int kLfPer = 16;  // rows per epilogue thread
+// Within +-kDeep; NaN stays NaN.
+__device__ __forceinline__ float clamp_deep(float d) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(d) : "f"(-kDeep));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(d) : "f"(kDeep));
+  return d;
+}
+
+template <int NH>
+struct FewShape {
+  static constexpr int kN = 32 * NH;
+  static constexpr int kStages = NH == 1 ? 10 : 8;
+  static constexpr uint32_t kWBytes = 128 * kLsBK * 2, kHBytes = kN * kLsBK * 2;
+  static constexpr uint32_t kStage = kWBytes + kHBytes;
+  static constexpr int kGroups = kN / kLfPer;  // of four warps each
+  static constexpr int kThreads = (2 + 4 * kGroups) * 32;
+  static constexpr uint32_t kCols = 2 * kN < 32 ? 32 : 2 * kN;
+  // stages, each row's log2(e) / T and token, the warps' sums, barriers
+  static constexpr uint32_t kC2 = kStages * kStage, kToken = kC2 + kN * 4,
+                            kJoin = kToken + kN * 4,
+                            kBars = kJoin + 4 * kN * 16, kSmem = kBars + 8 * (2 * kStages + 5) +
+                                                                16 + 1024;
+};
+
+template <int NH>
+__global__ void __launch_bounds__(FewShape<NH>::kThreads, 1)
+    lmfew_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_w,
+                 const LmScoreArgs p) {
+  using S = FewShape<NH>;
+  extern __shared__ unsigned char ls_smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(ls_smem_raw) + 1023) & ~(uintptr_t)1023);
+  float* row_c2 = reinterpret_cast<float*>(smem + S::kC2);
+  int* row_token = reinterpret_cast<int*>(smem + S::kToken);
+  float4* join = reinterpret_cast<float4*>(smem + S::kJoin);  // [4][kN]
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBars);
+  uint64_t* empty = full + S::kStages;
+  uint64_t* acc_full = empty + S::kStages;  // [2]
+  uint64_t* acc_empty = acc_full + 2;       // [2]
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n_nt = (p.V + 127) / 128;
+  const int nt_lo = (int)((long long)blockIdx.x * n_nt / p.n_split);
+  const int nt_hi = (int)((long long)(blockIdx.x + 1) * n_nt / p.n_split);
+  const int n_tiles = nt_hi - nt_lo;
+  const int KB = (p.d + kLsBK - 1) / kLsBK;
+
+  if (tid == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 4 * S::kGroups);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  for (int r = tid; r < S::kN; r += S::kThreads) {
+    row_token[r] = r < p.rows ? p.tokens[r] : -1;
+    row_c2[r] = r < p.rows ? kLog2e / lm_temp(p, r) : 1.f;
+  }
+  if (warp == 0) tc_alloc(tmem_slot, S::kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto fail = [&]() {
+    atomicOr(p.status, kScoreTimeout);
+    *(volatile int*)abort_flag = 1;
+  };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer
+    if (lane == 0) {
+      const uint64_t keep = evict_last_policy(), once = evict_first_policy();
+      int s = 0, issued = 0;
+      uint32_t phase = 1u;
+      bool ok = true;
+      for (int t = 0; t < n_tiles && ok; ++t) {
+        for (int kb = 0; kb < KB; ++kb, ++issued) {
+          if (!mbar_wait(&empty[s], phase, p.wait_ns, abort_flag)) {
+            fail();
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[s], S::kStage);
+          unsigned char* dst = smem + (uint32_t)s * S::kStage;
+          tma_load_2d(dst, &tm_w, kb * kLsBK, (nt_lo + t) * 128, &full[s], once);
+          tma_load_2d(dst + S::kWBytes, &tm_h, kb * kLsBK, 0, &full[s], keep);
+          if (++s == S::kStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // every copy issued has landed before the CTA may leave
+      for (int i = max(0, issued - S::kStages); i < issued; ++i)
+        mbar_wait(&full[i % S::kStages], (uint32_t)(i / S::kStages) & 1u, kDrainLimitNs);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = lm_idesc(128, S::kN);
+      const uint32_t base = smem_u32(smem);
+      int s = 0, used = 0;
+      uint32_t phase = 0u;
+      bool ok = true;
+      for (int t = 0; t < n_tiles && ok; ++t) {
+        for (int kb = 0; kb < KB && ok; ++kb) {
+          const int buf = used & 1, in_chunk = kb % kLsChunk;
+          if (in_chunk == 0 && used >= 2) {
+            if (!mbar_wait(&acc_empty[buf], (uint32_t)(used / 2 - 1) & 1u, p.wait_ns,
+                           abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
+          if (!mbar_wait(&full[s], phase, p.wait_ns, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = base + (uint32_t)s * S::kStage, b = a + S::kWBytes;
+#pragma unroll
+          for (int k = 0; k < kLsBK / 16; ++k)
+            tc_mma(tmem + (uint32_t)(buf * S::kN), sw128_desc(a + k * 32u), sw128_desc(b + k * 32u),
+                   idesc, (in_chunk | k) != 0 ? 1u : 0u);
+          tc_commit(&empty[s]);
+          if (++s == S::kStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+          if (in_chunk == kLsChunk - 1 || kb == KB - 1) {
+            tc_commit(&acc_full[buf]);
+            ++used;
+          }
+        }
+      }
+      if (!ok) fail();
+      tc_commit(drain);
+      mbar_wait(drain, 0u, kDrainLimitNs);
+    }
+  } else {
+    // --------------------------------------------------------- epilogue
+    const int q = warp & 3;            // TMEM lanes 32 q .. 32 q + 31
+    const int r0 = ((warp - 2) >> 2) * kLfPer;  // rows r0 ..
+    const int chunks = (KB + kLsChunk - 1) / kLsChunk;
+    const int n_rows = min(kLfPer, p.rows - r0);
+    float m[kLfPer], R[kLfPer], Q[kLfPer];
+#pragma unroll
+    for (int r = 0; r < kLfPer; ++r) {
+      m[r] = -FLT_MAX;
+      R[r] = Q[r] = 0.f;
+    }
+    int used = 0;
+    bool ok = true;
+    for (int t = 0; t < n_tiles && ok; ++t) {
+      float z[kLfPer];
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c, ++used) {
+        const int buf = used & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (uint32_t)(used / 2) & 1u,
+                                               p.wait_ns, abort_flag))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float v[kLfPer];
+        __syncwarp();  // tcgen05.ld is warp-wide: every lane, converged
+        tc_ld16(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * S::kN + r0), v);
+        tc_wait_ld();
+#pragma unroll
+        for (int r = 0; r < kLfPer; ++r) z[r] = c == 0 ? v[r] : z[r] + v[r];
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      }
+      if (!ok) break;
+      const int id0 = (nt_lo + t) * 128 + 32 * q, id = id0 + lane;
+      const float4* c4 = reinterpret_cast<const float4*>(row_c2 + r0);
+      // rare: a row's token among this warp's ids, ids past the vocabulary
+      const int tok = row_token[r0 + (lane & (kLfPer - 1))] - id0;
+      if (id0 + 32 > p.V || __any_sync(0xffffffffu, tok >= 0 && tok < 32)) {
+#pragma unroll
+        for (int r = 0; r < kLfPer; ++r) {
+          if (row_token[r0 + r] == id && id < p.V) {
+            p.za[r0 + r] = z[r];
+            z[r] = -INFINITY;
+          }
+          if (id >= p.V) z[r] = -INFINITY;
+        }
+      }
+      // every id is its own reference's next candidate, so new maxima are
+      // common: without a branch, one of the two factors being 1
+#pragma unroll
+      for (int r = 0; r < kLfPer; r += 4) {
+        const float4 c = c4[r / 4];
+        const float cr[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float x = z[r + k];
+          const float d = clamp_deep((x - m[r + k]) * cr[k]);
+          const bool up = d > 0.f;
+          const float f = ex2(-fabsf(d));
+          const float Qup = f * fmaf(-d, R[r + k], Q[r + k]);
+          Q[r + k] = up ? Qup : fmaf(f, d, Q[r + k]);
+          R[r + k] = up ? fmaf(R[r + k], f, 1.f) : R[r + k] + f;
+          m[r + k] = up ? x : m[r + k];
+        }
+      }
+    }
+    if (!ok && lane == 0) fail();
+#pragma unroll
+    for (int r = 0; r < kLfPer; ++r) {
+      if (r >= n_rows) break;
+      const RowSums w =
+          warp_join(RowSums{m[r], R[r], Q[r]}, row_c2[r0 + r]);
+      if (lane == 0) join[q * S::kN + r0 + r] = make_float4(w.m, w.R, w.Q, 0.f);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  for (int r = tid; r < p.rows; r += S::kThreads) {
+    const float c2 = row_c2[r];
+    RowSums s = row_sums_empty();
+    for (int q = 0; q < 4; ++q) {
+      const float4 v = join[q * S::kN + r];
+      s = row_sums_join(s, RowSums{v.x, v.y, v.z}, c2);
+    }
+    // a cut-short pass leaves NaN, not a part of the sums
+    if (*(volatile int*)abort_flag) s.R = __int_as_float(0x7fc00000);
+    p.sums[(size_t)blockIdx.x * (size_t)p.rows + (size_t)r] = s;
+  }
+  if (warp == 0) {
+    __syncwarp();
+    tc_dealloc(tmem, S::kCols);
+    tc_relinquish();
+  }
+}
+
+// A warp per row: the ranges' sums, then the row's results.  Launched as a
+// programmatic dependent: it waits for the product's kernel to complete.
 __global__ void __launch_bounds__(128) lmscore_finish_kernel(const LmScoreArgs p) {
   const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= p.rows) return;
   const int token = p.tokens[row];
+  const float c2 = kLog2e / lm_temp(p, row);
+  griddep_wait();
   if (token < 0) {
     if (lane == 0) {
       p.logprobs[row] = 0.f;
@@ -393,11 +664,22 @@ __global__ void __launch_bounds__(128) lmscore_finish_kernel(const LmScoreArgs p
     return;
   }
   const bool bad = token >= p.V;
-  const float za = bad ? __int_as_float(0x7fc00000) : p.za[row];
-  const float c2 = kLog2e / lm_temp(p, row);
+  const float za = bad ? __int_as_float(0x7fc00000) : __ldcg(p.za + row);
   RowSums s = row_sums_empty();
-  for (int k = lane; k < 2 * p.n_split; k += 32)
-    s = row_sums_join(s, p.sums[(size_t)k * (size_t)p.rows + (size_t)row], c2);
+  for (int k0 = lane; k0 < p.n_rec; k0 += 5 * 32) {
+    RowSums v[5];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) {
+      const int k = k0 + 32 * j;
+      v[j] = row_sums_empty();
+      if (k < p.n_rec) {
+        const float* r = reinterpret_cast<const float*>(p.sums + (size_t)k * (size_t)p.rows + row);
+        v[j] = RowSums{__ldcg(r), __ldcg(r + 1), __ldcg(r + 2)};
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 5; ++j) s = row_sums_join(s, v[j], c2);
+  }
   s = warp_join(s, c2);
   const RowResult r = row_result(s, za, c2);
   if (lane != 0) return;

@@ -375,23 +375,6 @@ void fill_args(const eb_sampler* h, StepArgs& a, int step) {
   a.key1 = (uint32_t)(c.seed >> 32);
 }
 
-// A kernel launched as a programmatic dependent of the previous one on `st`.
-int launch_dependent(const void* fn, dim3 grid, dim3 block, size_t smem, void** args,
-                     cudaStream_t st) {
-  cudaLaunchConfig_t lc;
-  std::memset(&lc, 0, sizeof(lc));
-  lc.gridDim = grid;
-  lc.blockDim = block;
-  lc.dynamicSmemBytes = smem;
-  lc.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelExC(&lc, fn, args) == cudaSuccess ? EB_OK : EB_ERR_CUDA;
-}
-
 // The stream kernel over `logits` (this device's rows or vocabulary slice),
 // a programmatic dependent of the stream's previous kernel.
 int launch_stream(const KernelCfg& kc, StepArgs& a, const void* logits, int dtype, size_t V,
@@ -401,8 +384,10 @@ int launch_stream(const KernelCfg& kc, StepArgs& a, const void* logits, int dtyp
   a.vec_ok = ((uintptr_t)logits % 16 == 0) && ((V * elt) % 16 == 0) ? 1 : 0;
   a.G1 = kc.grid;
   void* args[] = {&a};
-  return launch_dependent(kc.fn, dim3(kc.grid), dim3(ebk::stream_threads(dtype)), kc.smem, args,
-                          st);
+  return ebk::launch_dependent(kc.fn, dim3(kc.grid), dim3(ebk::stream_threads(dtype)), kc.smem,
+                               args, st)
+             ? EB_OK
+             : EB_ERR_CUDA;
 }
 
 bool is_slice(const eb_sampler* h) {

@@ -78,11 +78,22 @@ void info_setup(DeviceInfo& d, int device) {
     d.rc = EB_ERR_UNSUPPORTED;
     return;
   }
-  if (cudaFuncSetAttribute(ebk::lmscore_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           optin) != cudaSuccess) {
-    cudaGetLastError();
-    d.rc = EB_ERR_CUDA;
-    return;
+  const int lm_smem[3] = {(int)ebk::lm_score_layout().total, (int)ebk::FewShape<1>::kSmem,
+                          (int)ebk::FewShape<2>::kSmem};
+  const void* lm_fn[3] = {reinterpret_cast<const void*>(&ebk::lmscore_kernel),
+                          reinterpret_cast<const void*>(&ebk::lmfew_kernel<1>),
+                          reinterpret_cast<const void*>(&ebk::lmfew_kernel<2>)};
+  for (int k = 0; k < 3; ++k) {
+    if (lm_smem[k] > optin) {
+      d.rc = EB_ERR_UNSUPPORTED;
+      return;
+    }
+    if (cudaFuncSetAttribute(lm_fn[k], cudaFuncAttributeMaxDynamicSharedMemorySize, lm_smem[k]) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      d.rc = EB_ERR_CUDA;
+      return;
+    }
   }
   const uint32_t ring_smem = ebk::ring_layout(kRingStages).total;
   if (ring_smem > (uint32_t)optin) {
@@ -499,23 +510,42 @@ int eb_lmhead_logprobs(eb_scorer_t* h, const void* hidden, const void* weight, i
   p.rows = rows;
   p.V = V;
   p.d = d;
-  p.n_split = ebk::lm_score_split(h->sms, rows, V);
   p.wait_ns = h->wait_ns;
   p.status = h->status;
   p.logprobs = logprobs;
   p.entropies = entropies;
-  if (2 * (size_t)p.n_split * (size_t)rows > h->lm_slots) return EB_ERR_OVERFLOW;
+  const bool few = rows <= ebk::kLfRows;
+  if (few) {
+    p.n_split = std::min(h->sms, (V + 127) / 128);
+    p.n_rec = p.n_split;
+  } else {
+    p.n_split = ebk::lm_score_split(h->sms, rows, V);
+    p.n_rec = 2 * p.n_split;
+  }
+  if ((size_t)p.n_rec * (size_t)rows > h->lm_slots) return EB_ERR_OVERFLOW;
+  const bool wide = rows > 32;  // of the few: 64 columns
   CUtensorMap th, tw;
-  if (!ebk::make_tmap(&th, hidden, (uint64_t)d, (uint64_t)rows, ebk::kLsBK, ebk::kLsRows) ||
-      !ebk::make_tmap(&tw, weight, (uint64_t)d, (uint64_t)V, ebk::kLsBK, ebk::kLsHalf))
+  if (!ebk::make_tmap(&th, hidden, (uint64_t)d, (uint64_t)rows, ebk::kLsBK,
+                      !few ? ebk::kLsRows : wide ? 64 : 32) ||
+      !ebk::make_tmap(&tw, weight, (uint64_t)d, (uint64_t)V, ebk::kLsBK, 128))
     return EB_ERR_CUDA;
-  const size_t smem = ebk::lm_score_layout().total;
-  if (smem > h->optin) return EB_ERR_UNSUPPORTED;
-  const int n_mt = (rows + ebk::kLsBM - 1) / ebk::kLsBM;
-  ebk::lmscore_kernel<<<2 * n_mt * p.n_split, ebk::kLsThreads, smem, st>>>(th, tw, p);
+  if (!few) {
+    const int n_mt = (rows + ebk::kLsBM - 1) / ebk::kLsBM;
+    ebk::lmscore_kernel<<<2 * n_mt * p.n_split, ebk::kLsThreads, ebk::lm_score_layout().total,
+                          st>>>(th, tw, p);
+  } else if (wide) {
+    ebk::lmfew_kernel<2><<<p.n_split, ebk::FewShape<2>::kThreads, ebk::FewShape<2>::kSmem, st>>>(
+        th, tw, p);
+  } else {
+    ebk::lmfew_kernel<1><<<p.n_split, ebk::FewShape<1>::kThreads, ebk::FewShape<1>::kSmem, st>>>(
+        th, tw, p);
+  }
   if (cudaGetLastError() != cudaSuccess) return EB_ERR_CUDA;
-  ebk::lmscore_finish_kernel<<<(rows + 3) / 4, 128, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? EB_OK : EB_ERR_CUDA;
+  void* args[] = {&p};
+  return ebk::launch_dependent(reinterpret_cast<const void*>(&ebk::lmscore_finish_kernel),
+                               dim3((rows + 3) / 4), dim3(128), 0, args, st)
+             ? EB_OK
+             : EB_ERR_CUDA;
 }
 
 int eb_scorer_status(eb_scorer_t* h, uint32_t* status, int clear, void* stream) {
