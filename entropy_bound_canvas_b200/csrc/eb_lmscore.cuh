@@ -304,7 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLsThreads, 1)
     const int row = row0 + 32 * q + lane;
     const bool valid = row < p.rows;
     const int token = valid ? p.tokens[row] : -1;
-    const float c2 = valid ? kLog2e / lm_temp(p, row) : 1.f;
+    const float c2 = valid ? log2e_over(lm_temp(p, row)) : 1.f;
     const uint32_t free_bar[2] = {map_rank(smem_u32(&acc_empty[0]), 0),
                                   map_rank(smem_u32(&acc_empty[1]), 0)};
     const int chunks = (KB + kLsChunk - 1) / kLsChunk;
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(FewShape<NH>::kThreads, 1)
   }
   for (int r = tid; r < S::kN; r += S::kThreads) {
     row_token[r] = r < p.rows ? p.tokens[r] : -1;
-    row_c2[r] = r < p.rows ? kLog2e / lm_temp(p, r) : 1.f;
+    row_c2[r] = r < p.rows ? log2e_over(lm_temp(p, r)) : 1.f;
   }
   if (warp == 0) tc_alloc(tmem_slot, S::kCols);
   tc_fence_before();
@@ -654,7 +654,8 @@ __global__ void __launch_bounds__(128) lmscore_finish_kernel(const LmScoreArgs p
   const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= p.rows) return;
   const int token = p.tokens[row];
-  const float c2 = kLog2e / lm_temp(p, row);
+  const Scale sc = row_scale(lm_temp(p, row));
+  const float c2 = sc.c2;
   griddep_wait();
   if (token < 0) {
     if (lane == 0) {
@@ -681,7 +682,7 @@ __global__ void __launch_bounds__(128) lmscore_finish_kernel(const LmScoreArgs p
     for (int j = 0; j < 5; ++j) s = row_sums_join(s, v[j], c2);
   }
   s = warp_join(s, c2);
-  const RowResult r = row_result(s, za, c2);
+  const RowResult r = row_result<true>(s, za, sc);
   if (lane != 0) return;
   p.logprobs[row] = r.lp;
   if (p.entropies) p.entropies[row] = r.H;

@@ -37,9 +37,28 @@ constexpr uint32_t kScoreBadToken = 1u, kScoreNonFinite = 2u, kScoreTimeout = 4u
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 // Terms below 2^-kDeep of the maximum are zero in fp32 with flush to zero;
-// clamping their exponent keeps e d = 0 where d would be -inf (a logit of
+// holding their exponent there keeps e d = 0 where d would be -inf (a logit of
 // -inf, or one whose distance to the maximum overflows).
 constexpr float kDeep = 200.0f;
+// NaN stays NaN.
+__device__ __forceinline__ float hold_deep(float d) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(d), "f"(-kDeep));
+  return r;
+}
+__device__ __forceinline__ bool row_temp_ok(float T) { return T > 0.f && T < INFINITY; }
+// log2(e) / T, rounded once or nearly so, and what that left.
+struct Scale {
+  float c2, low;
+};
+__device__ __forceinline__ Scale row_scale(float T) {
+  const float r = __frcp_rn(T), q = kLog2e * r;
+  // log2(e) is kLog2e in fp32 plus 1.92596e-8
+  constexpr float kLog2eLow = 1.925963033500e-8f;
+  const float c2 = fmaf(fmaf(-q, T, kLog2e) + kLog2eLow, r, q);
+  return Scale{c2, (fmaf(-c2, T, kLog2e) + kLog2eLow) * r};
+}
+__device__ __forceinline__ float log2e_over(float T) { return row_scale(T).c2; }
 
 struct ScoreArgs {
   const void* logits;  // [rows][ld]
@@ -129,49 +148,72 @@ __device__ __forceinline__ RowSums row_sums_shuffle(RowSums s, int mask, float c
 }
 
 struct RowResult {
-  float M;     // maximum over every logit
-  float l2S;   // log2 S
-  float lp;    // log p_a (nats)
-  float H;     // entropy (nats)
-  float rest;  // 1 - p_a
-  float pa;    // p_a
+  float M;             // maximum over every logit (or near it, see kLazy)
+  float l2S, l2S_low;  // log2 S, and what its rounding left
+  float lp, lp_low;    // log p_a (nats), and what its rounding left
+  float H;             // entropy (nats)
+  float rest;          // 1 - p_a
+  float pa;            // p_a
   bool finite;
 };
 
 // s: the sums without the token; za: the token's logit (NaN: a bad token).
-__device__ __forceinline__ RowResult row_result(RowSums s, float za, float c2) {
+// log2 S is kept as a + b, a an integer or d_a and b small, so that the
+// differences log p_a and H round only their own size.  ENT: Q is there; it
+// also takes out the rounding of c2, by d log2 S / d c2 = (Q + e_a d_a) / (S c2).
+template <bool ENT>
+__device__ __forceinline__ RowResult row_result(RowSums s, float za, Scale sc) {
+  const float c2 = sc.c2;
   RowResult r;
   const float M = fmaxf(s.m, za);
   const float ds = fmaxf((s.m - M) * c2, -kDeep);
   const float fs = ex2(ds);
   const float R = s.R * fs;
   const float Q = fs * fmaf(ds, s.R, s.Q);
-  const float da = (za - M) * c2;
+  const float gap = za - M, da = gap * c2, da_low = fmaf(gap, c2, -da);
   const float ea = ex2(da);
   const float S = R + ea;
-  float lnS;
-  if (ea >= R) {
-    const float t = log1pf(__fdividef(R, ea));
-    lnS = fmaf(da, kLn2, t);
-    r.lp = -t;
-  } else {
-    lnS = logf(S);
-    r.lp = fmaf(da, kLn2, -lnS);
-  }
-  r.M = M;
-  r.l2S = lnS * kLog2e;
+  r.finite = S > 0.f && S < INFINITY;
   // e_a = 0: no entropy term, whatever d_a
   const float W = ea == 0.f ? Q : fmaf(ea, da, Q);
   const float iS = __frcp_rn(S);
-  r.H = fmaf(-kLn2, W * iS, lnS);
+  const float w = W * iS;
+  float a, b;
+  if (ea >= R) {
+    const float t = log1pf(__fdividef(R, ea));
+    a = da;
+    b = t * kLog2e;
+    r.lp = -t;
+    r.lp_low = 0.f;
+  } else {
+    // S = 2^k f, f in [1/sqrt 2, sqrt 2)
+    const int k = (int)((__float_as_uint(S) + 0x004afb0du) >> 23) - 127;
+    a = (float)k;
+    b = log2f(S * __uint_as_float((uint32_t)(127 - k) << 23));
+    // ln 2 (d_a - a - b), the low parts kept (two-sums and a two-product)
+    const float s1 = da - a, u = s1 - da, e1 = (da - (s1 - u)) - (a + u);
+    const float s2 = s1 - b, v = s2 - s1, e2 = (s1 - (s2 - v)) - (b + v);
+    float low = e1 + e2 + da_low;
+    if (ENT) low += sc.low * (gap - w / c2);
+    constexpr float kLn2Low = -1.904654323148236e-9f;  // ln 2 - kLn2
+    r.lp = kLn2 * s2;
+    r.lp_low = fmaf(kLn2, s2, -r.lp) + fmaf(kLn2, low, kLn2Low * s2);
+    if (!(r.lp > -INFINITY)) r.lp_low = 0.f;  // a banned token
+    const float sum = r.lp + r.lp_low;
+    r.lp_low = r.lp_low - (sum - r.lp);
+    r.lp = sum;
+    if (!(r.lp > -INFINITY)) r.lp_low = 0.f;
+  }
+  r.M = M;
+  r.l2S = a + b;
+  r.l2S_low = (a - r.l2S) + b;
+  const float w_low = fmaf(-w, S, W) * iS;
+  r.H = kLn2 * (((a - w) - w_low) + b);
   r.rest = R / S;
   r.pa = ea * iS;
-  r.finite = S > 0.f && S < INFINITY;
-  if (!r.finite) r.lp = r.H = r.l2S = r.rest = r.pa = __int_as_float(0x7fc00000);
+  if (!r.finite) r.lp = r.lp_low = r.H = r.l2S = r.rest = r.pa = __int_as_float(0x7fc00000);
   return r;
 }
-
-__device__ __forceinline__ bool row_temp_ok(float T) { return T > 0.f && T < INFINITY; }
 
 struct RowCoef {
   float g, h;  // upstream gradients of log p_a and H
@@ -187,11 +229,13 @@ struct RowGrad {
 template <bool ENT>
 __device__ __forceinline__ RowGrad row_grad(const RowResult& r, RowCoef c, float T) {
   const float iT = 1.f / T;
+  // p = 2^(d - l2S) 2^-l2S_low: the second factor goes into the coefficients
+  const float f = fmaf(-kLn2, r.l2S_low, 1.f) * -iT;
   RowGrad o;
   o.M = r.M;
   o.l2S = r.l2S;
-  o.a0 = -iT * (ENT ? fmaf(c.h, r.H, c.g) : c.g);
-  o.a1 = -iT * c.h * kLn2;
+  o.a0 = f * (ENT ? fmaf(c.h, r.H, c.g) : c.g);
+  o.a1 = f * c.h * kLn2;
   // p_a = 0: log p_a may be -inf, its entropy term is 0
   const float ha = !ENT ? 0.f : r.pa > 0.f ? c.h * r.pa * (r.lp + r.H) : r.pa;
   o.own = iT * (c.g * r.rest - ha);
@@ -221,7 +265,7 @@ struct PolicyRow {
 
 __device__ __forceinline__ PolicyRow policy_row(const ScoreArgs& p, const RowResult& r,
                                                 float old_lp, float adv, float ref_lp) {
-  const float ratio = expf(r.lp - old_lp);
+  const float ratio = expf((r.lp - old_lp) + r.lp_low);
   const float free = -adv * ratio;
   // the comparisons keep a NaN ratio NaN
   const float held_ratio = ratio < p.clip_lo ? p.clip_lo : ratio > p.clip_hi ? p.clip_hi : ratio;
@@ -231,7 +275,7 @@ __device__ __forceinline__ PolicyRow policy_row(const ScoreArgs& p, const RowRes
   o.pg = o.cut ? held : free;
   o.kl = o.dkl = 0.f;
   if (p.ref_lp) {
-    const float gap = ref_lp - r.lp;
+    const float gap = (ref_lp - r.lp) - r.lp_low;
     const float back = expm1f(gap);
     o.kl = back - gap;
     o.dkl = -back;
@@ -546,11 +590,10 @@ __device__ __forceinline__ float pair_sum(const uint64_t (&v)[2]) {
   return a + b;
 }
 
-// Sums of N granules against the reference m.  CLAMP: exponents are held at
-// -kDeep (e = 0 there), and `low` gets a bit for each granule that needed it.
-template <int DT, bool ENT, bool CLAMP, int N>
+// Sums of N granules against the reference m.
+template <int DT, bool ENT, int N>
 __device__ __forceinline__ void granule_sums(const uint4 (&w)[N], float m, float c2,
-                                             uint64_t (&R)[2], uint64_t (&Q)[2], unsigned& low) {
+                                             uint64_t (&R)[2], uint64_t (&Q)[2]) {
   const uint64_t cc = pack2(c2, c2);
   R[0] = R[1] = Q[0] = Q[1] = 0ull;
 #pragma unroll
@@ -561,10 +604,9 @@ __device__ __forceinline__ void granule_sums(const uint4 (&w)[N], float m, float
       uint64_t d = mul2(v.v[k], cc);
       float d0, d1;
       unpack2(d, d0, d1);
-      if (CLAMP) {  // by comparison, so that NaN stays NaN
-        if (d0 < -kDeep || d1 < -kDeep) low |= 1u << n;
-        d0 = d0 < -kDeep ? -kDeep : d0;
-        d1 = d1 < -kDeep ? -kDeep : d1;
+      if (ENT) {
+        d0 = hold_deep(d0);
+        d1 = hold_deep(d1);
         d = pack2(d0, d1);
       }
       const uint64_t e = pack2(ex2(d0), ex2(d1));
@@ -591,39 +633,13 @@ __device__ __forceinline__ void raise(ThreadSums& s, const uint4 (&w)[N], float 
 }
 
 // Folds N granules into a thread's sums.  `drop`: the element that is left out
-// (counted through the N granules), or -1; its value goes to `za`.  `low`: the
-// granules with elements so far below the reference that their exponent has
-// to be clamped.
+// (counted through the N granules), or -1; its value goes to `za`.
 template <int DT, bool ENT, int N>
-__device__ __forceinline__ void fold(ThreadSums& s, uint4 (&w)[N], int drop, float c2, float& za,
-                                     unsigned& low) {
+__device__ __forceinline__ void fold(ThreadSums& s, uint4 (&w)[N], int drop, float c2, float& za) {
+  if (drop >= 0) za = granule_drop<DT, N>(w, drop);
   raise<DT, ENT, N>(s, w, c2);
   uint64_t R[2], Q[2];
-  granule_sums<DT, ENT, false, N>(w, s.m, c2, R, Q, low);
-  bool again = drop >= 0;
-  if (ENT) {  // an exponent of -inf makes e d NaN
-    const float t = pair_sum(Q);
-    again = again || t != t;
-  }
-  if (again) {
-    if (drop >= 0) za = granule_drop<DT, N>(w, drop);
-    granule_sums<DT, ENT, true, N>(w, s.m, c2, R, Q, low);
-  }
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    s.R[k] = add2(s.R[k], R[k]);
-    if (ENT) s.Q[k] = add2(s.Q[k], Q[k]);
-  }
-}
-
-// fold for granules that may hold places outside the row (-inf): always with
-// the clamp.
-template <int DT, bool ENT, int N>
-__device__ __forceinline__ void fold_clamped(ThreadSums& s, const uint4 (&w)[N], float c2,
-                                             unsigned& low) {
-  raise<DT, ENT, N>(s, w, c2);
-  uint64_t R[2], Q[2];
-  granule_sums<DT, ENT, true, N>(w, s.m, c2, R, Q, low);
+  granule_sums<DT, ENT, N>(w, s.m, c2, R, Q);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     s.R[k] = add2(s.R[k], R[k]);
@@ -632,7 +648,7 @@ __device__ __forceinline__ void fold_clamped(ThreadSums& s, const uint4 (&w)[N],
 }
 
 // The gradient p (a0 + a1 log2 p), p = 2^((z - M) c2 - l2S), of a granule.
-template <int DT, bool ENT, bool CLAMP>
+template <int DT, bool ENT>
 __device__ __forceinline__ void granule_grad(const uint4& w, float M, uint64_t c2, uint64_t nl,
                                              uint64_t A0, uint64_t A1,
                                              float (&o)[ScoreType<DT>::kPer16]) {
@@ -642,9 +658,9 @@ __device__ __forceinline__ void granule_grad(const uint4& w, float M, uint64_t c
     uint64_t x = fma2(z.v[k], c2, nl);
     float xa, xb;
     unpack2(x, xa, xb);
-    if (ENT && CLAMP) {
-      xa = xa < -kDeep ? -kDeep : xa;
-      xb = xb < -kDeep ? -kDeep : xb;
+    if (ENT) {
+      xa = hold_deep(xa);
+      xb = hold_deep(xb);
       x = pack2(xa, xb);
     }
     const uint64_t e = pack2(ex2(xa), ex2(xb));
@@ -880,7 +896,8 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
           continue;
         }
         const uint32_t par = count % kSlots, ph = (count / kSlots) & 1u;
-        const float c2 = kLog2e / Trow;
+        const Scale sc = row_scale(Trow);
+        const float c2 = sc.c2;
         if (lane == 0) mbar_arrive_expect_tx(&sums_in[par], (uint32_t)(C * NW * 16));
         __syncwarp();
         if (!wait(&sums_in[par], ph)) {
@@ -919,7 +936,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
           if (lane < C) arrive_remote(map_rank(smem_u32(&result[par]), lane));
         }
         const bool bad = a >= p.V;
-        const RowResult r = row_result(all, bad ? nan : za, c2);
+        const RowResult r = row_result<ENT>(all, bad ? nan : za, sc);
         RowCoef c{y0, y1};
         PolicyRow o{};
         if (q.mode == kModePolicy) {
@@ -953,9 +970,8 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
     // A folded row whose gradient is still to be written.
     struct Pending {
       int row, token;
-      float c2, m;
-      bool deep;
-    } last{-1, 0, 0.f, 0.f, false};
+      float c2;
+    } last{-1, 0, 0.f};
 
     // The token's place in this CTA's share: this thread's granule (counted
     // along its own granules, -1: another thread's) and element.
@@ -984,7 +1000,6 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
       const int mine = place(sh, w.token, el);
       const float c2 = w.c2;
       const uint64_t cc = pack2(c2, c2), nl = pack2(-r.l2S, -r.l2S), A0 = pack2(r.a0, r.a0), A1 = pack2(r.a1, r.a1);
-      const bool deep = w.deep || (ENT && (w.m - r.M) * c2 < -kDeep);
       const int n_st = (sh.n + kStageGran - 1) / kStageGran;
       if (!q.ahead) walk.turn();
       for (int i = 0; i < n_st; ++i) {
@@ -1000,8 +1015,8 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
         const uint4* st = reinterpret_cast<const uint4*>(ring + (size_t)at * kStageBytes) + tid;
         const int n = sh.n - st_no * kStageGran, first = st_no * kIter;
         const int g = sh.g0 + st_no * kStageGran + tid;
-        // a stage of whole granules without the token, nothing to clamp
-        const bool plain = (kIter - 1) * kT + tid < n && dz_vec && !deep &&
+        // a stage of whole granules without the token
+        const bool plain = (kIter - 1) * kT + tid < n && dz_vec &&
                            (unsigned)(mine - first) >= (unsigned)kIter && g >= sh.whole0 &&
                            g + (kIter - 1) * kT < sh.whole1;
         if (plain) {
@@ -1009,7 +1024,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
 #pragma unroll
           for (int j = 0; j < kIter; ++j) {
             float o[kPer];
-            granule_grad<DT, ENT, false>(st[j * kT], r.M, cc, nl, A0, A1, o);
+            granule_grad<DT, ENT>(st[j * kT], r.M, cc, nl, A0, A1, o);
             store_stream(out + j * kT, granule_pack<DT>(o));
           }
         } else {
@@ -1017,7 +1032,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
           for (int j = 0; j < kIter && j * kT + tid < n; ++j) {
             const int gj = g + j * kT;
             float o[kPer];
-            granule_grad<DT, ENT, true>(st[j * kT], r.M, cc, nl, A0, A1, o);
+            granule_grad<DT, ENT>(st[j * kT], r.M, cc, nl, A0, A1, o);
             if (first + j == mine) {
 #pragma unroll
               for (int k = 0; k < kPer; ++k)
@@ -1055,7 +1070,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
       const int row = row_of(i);
       const int a = token;
       const float wt = weight;
-      const float c2 = kLog2e / (row_temp_ok(T) ? T : nan);
+      const float c2 = log2e_over(row_temp_ok(T) ? T : nan);
       if (i + ncl < p.rows) {
         token = p.tokens[row_of(i + ncl)];
         if (p.weights) weight = p.weights[row_of(i + ncl)];
@@ -1087,7 +1102,6 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
       ThreadSums s;
       s.m = -FLT_MAX;
       s.R[0] = s.R[1] = s.Q[0] = s.Q[1] = 0ull;
-      bool deep = false;
       float za = 0.f;
       const int n_st = (sh.n + kStageGran - 1) / kStageGran;
       // stages that stay for the gradient: all (ahead), or the last ones
@@ -1103,33 +1117,19 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
         const int n = sh.n - k * kStageGran, first = k * kIter;
         const int drop =
             (unsigned)(mine - first) < (unsigned)kIter ? (mine - first) * kPer + el : -1;
-        unsigned low = 0u;
-        const int g = sh.g0 + first * kT + tid;
         if ((kIter - 1) * kT + tid < n) {
           uint4 w[kIter];
 #pragma unroll
           for (int j = 0; j < kIter; ++j) w[j] = st[j * kT];
-          fold<DT, ENT, kIter>(s, w, drop, c2, za, low);
+          fold<DT, ENT, kIter>(s, w, drop, c2, za);
         } else {
           // past the share's end: what is left, one granule at a time
 #pragma unroll 1
           for (int j = 0; j < kIter - 1 && j * kT + tid < n; ++j) {
             uint4 w[1] = {st[j * kT]};
-            unsigned l = 0u;
             fold<DT, ENT, 1>(s, w, drop >= j * kPer && drop < (j + 1) * kPer ? drop - j * kPer : -1,
-                             c2, za, l);
-            low |= l << j;
+                             c2, za);
           }
-        }
-        // Elements far below the reference need the clamp again for their
-        // gradient.  The granules that the row fills in part and the token's
-        // own have it anyway.
-        if (GRAD && low) {
-#pragma unroll
-          for (int j = 0; j < kIter; ++j)
-            if ((low >> j & 1u) && first + j != mine && g + j * kT >= sh.whole0 &&
-                g + j * kT < sh.whole1)
-              deep = true;
         }
         if (k < n_st - stay) {
           __syncwarp();
@@ -1158,7 +1158,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
                   map_rank(smem_u32(&sums_in[par]), lane));
       }
       if (GRAD) {
-        const Pending now{row, a, c2, s.m, deep};
+        const Pending now{row, a, c2};
         if (!q.ahead)
           write_grad(now, count);
         else if (last.row >= 0)
@@ -1290,7 +1290,8 @@ __global__ void __launch_bounds__(kShortThreads, GRAD ? 6 : 8)
       x0 = p.g_lp[row];
       if (p.g_h) x1 = p.g_h[row];
     }
-    const float c2 = kLog2e / T;
+    const Scale sc = row_scale(T);
+    const float c2 = sc.c2;
     const bool bad = token >= p.V;
     const int at = token + sh.shift, ag = at / kPer, el = at & (kPer - 1);
     const int mine = !bad && ag % kT == tid ? ag / kT : -1;
@@ -1305,9 +1306,7 @@ __global__ void __launch_bounds__(kShortThreads, GRAD ? 6 : 8)
 #pragma unroll
       for (int k = 0; k < kShortChunk; ++k) v[k] = w[c][k];
       const int j = mine - c * kShortChunk;
-      if (j >= 0 && j < kShortChunk) za = granule_drop<DT, kShortChunk>(v, j * kPer + el);
-      unsigned low = 0u;
-      fold_clamped<DT, ENT, kShortChunk>(s, v, c2, low);
+      fold<DT, ENT, kShortChunk>(s, v, j >= 0 && j < kShortChunk ? j * kPer + el : -1, c2, za);
     }
     RowSums all = warp_join(RowSums{s.m, pair_sum(s.R), ENT ? pair_sum(s.Q) : 0.f}, c2);
     const unsigned holder = __ballot_sync(0xffffffffu, mine >= 0);
@@ -1325,7 +1324,7 @@ __global__ void __launch_bounds__(kShortThreads, GRAD ? 6 : 8)
       }
       flip ^= 1;  // the next row's sums do not meet a slow reader of these
     }
-    const RowResult r = row_result(all, bad ? nan : za, c2);
+    const RowResult r = row_result<ENT>(all, bad ? nan : za, sc);
     RowCoef c{x0, x1};
     if (mode == kModePolicy) {
       const PolicyRow o = policy_row(p, r, x0, x1, x2);
@@ -1346,7 +1345,7 @@ __global__ void __launch_bounds__(kShortThreads, GRAD ? 6 : 8)
         const int g = c1 * kT + tid;
         if (g >= sh.n) break;
         float o[kPer];
-        granule_grad<DT, ENT, true>(w[c1 / kShortChunk][c1 % kShortChunk], f.M, cc, nl, A0, A1, o);
+        granule_grad<DT, ENT>(w[c1 / kShortChunk][c1 % kShortChunk], f.M, cc, nl, A0, A1, o);
         if (c1 == mine) {
 #pragma unroll
           for (int k = 0; k < kPer; ++k)
