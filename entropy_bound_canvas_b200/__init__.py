@@ -516,10 +516,14 @@ class EBScorer:
         _check(_lib().eb_scorer_init(C.byref(h), self.max_rows, self.device.index),
                "eb_scorer_init")
         self._h = h
+        self._f32 = torch.empty((0,), dtype=torch.float32, device=self.device)
+        # the stream's handle without a Stream object, where torch offers it
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._raw_stream = raw or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
     # -- helpers --------------------------------------------------------------
     def _stream(self):
-        return _torch().cuda.current_stream(self.device).cuda_stream
+        return self._raw_stream(self.device.index)
 
     def _vector(self, t, n, dtype, name):
         """Address of a contiguous tensor of n values (None: a null pointer)."""
@@ -579,15 +583,14 @@ class EBScorer:
         """(gradient tensor shaped as the logits, its address, its row stride)."""
         torch = _torch()
         if out is None:
-            out = torch.empty(logits.shape, dtype=logits.dtype, device=self.device)
+            out = torch.empty_like(logits, memory_format=torch.contiguous_format)
         elif out.shape != logits.shape or out.dtype != logits.dtype:
             raise ValueError("out must have the logits' shape and type")
         d, ldd = self._matrix(out, "out")
         return out, d.data_ptr(), ldd
 
     def _new(self, n):
-        torch = _torch()
-        return torch.empty((n,), dtype=torch.float32, device=self.device)
+        return self._f32.new_empty((n,))
 
     # -- calls ------------------------------------------------------------------
     def token_logprobs(self, logits, tokens, temperature=1.0, entropies: bool = True):

@@ -129,6 +129,7 @@ struct eb_scorer {
   double* part = nullptr;           // [kMaxGrid][terms]
   float* lp = nullptr;              // [max_rows] log-probabilities (preference)
   float* g = nullptr;               // [max_rows] their gradients (preference)
+  float4* stats = nullptr;          // [max_rows] the rows' statistics (preference)
   ebk::LmSums* lm = nullptr;        // [lm_slots] the LM-head pass's partial sums
   float* lm_za = nullptr;           // [max_rows] the tokens' logits
   size_t lm_slots = 0;
@@ -260,7 +261,7 @@ int ring_log2C(const eb_scorer* h, int variant, bool f32, bool grad, int64_t row
 }
 
 int launch_rows(const eb_scorer* h, const ScoreArgs& a, int dtype, int mode, bool ent, bool grad,
-                bool reverse, cudaStream_t st) {
+                cudaStream_t st) {
   const int v = (dtype == EB_BF16 ? 4 : 0) + (ent ? 2 : 0) + (grad ? 1 : 0);
   const int64_t row_bytes = (int64_t)a.V * (int64_t)elt_bytes(dtype);
   // the aligned image of a row holds a granule more where rows start off 16 bytes
@@ -274,8 +275,8 @@ int launch_rows(const eb_scorer* h, const ScoreArgs& a, int dtype, int mode, boo
     const int per_block = wide ? 1 : 4;
     const int blocks = (int)std::min<int64_t>(((int64_t)a.rows + per_block - 1) / per_block,
                                               (int64_t)h->sms * (grad ? 6 : 8));
-    int m = mode, r = reverse ? 1 : 0;
-    void* args[] = {const_cast<ScoreArgs*>(&a), &m, &r};
+    int m = mode;
+    void* args[] = {const_cast<ScoreArgs*>(&a), &m};
     return cudaLaunchKernel(kShort[wide][v], dim3(std::max(1, blocks)), dim3(ebk::kShortThreads),
                             args, 0, st) == cudaSuccess
                ? EB_OK
@@ -286,7 +287,6 @@ int launch_rows(const eb_scorer* h, const ScoreArgs& a, int dtype, int mode, boo
   if (most < 1) return EB_ERR_CUDA;
   ebk::RingArgs q;
   q.mode = mode;
-  q.reverse = reverse ? 1 : 0;
   q.log2C = c;
   q.stages = kRingStages;
   q.ahead = 2 * share_stages(row_bytes, c) <= kRingStages;
@@ -333,6 +333,8 @@ int eb_scorer_init(eb_scorer_t** out, int32_t max_rows, int device) {
   off = align256(off + sizeof(float) * (size_t)max_rows);
   const size_t o_g = off;
   off = align256(off + sizeof(float) * (size_t)max_rows);
+  const size_t o_stats = off;
+  off = align256(off + sizeof(float4) * (size_t)max_rows);
   const size_t o_lm = off;
   off = align256(off + sizeof(ebk::LmSums) * h->lm_slots);
   const size_t o_za = off;
@@ -354,6 +356,7 @@ int eb_scorer_init(eb_scorer_t** out, int32_t max_rows, int device) {
   h->part = reinterpret_cast<double*>(base + o_part);
   h->lp = reinterpret_cast<float*>(base + o_lp);
   h->g = reinterpret_cast<float*>(base + o_g);
+  h->stats = reinterpret_cast<float4*>(base + o_stats);
   h->lm = reinterpret_cast<ebk::LmSums*>(base + o_lm);
   h->lm_za = reinterpret_cast<float*>(base + o_za);
   *out = h;
@@ -372,7 +375,7 @@ int eb_token_logprobs(eb_scorer_t* h, const eb_score_input_t* in, float* logprob
   fill_args(h, in, a);
   a.logprobs = logprobs;
   a.entropies = entropies;
-  return launch_rows(h, a, in->dtype, ebk::kModeScore, entropies != nullptr, false, false,
+  return launch_rows(h, a, in->dtype, ebk::kModeScore, entropies != nullptr, false,
                      (cudaStream_t)stream);
 }
 
@@ -392,7 +395,7 @@ int eb_token_logprobs_backward(eb_scorer_t* h, const eb_score_input_t* in,
   a.ldd = ldd;
   a.g_lp = d_logprobs;
   a.g_h = d_entropies;
-  return launch_rows(h, a, in->dtype, ebk::kModeGrad, d_entropies != nullptr, true, false,
+  return launch_rows(h, a, in->dtype, ebk::kModeGrad, d_entropies != nullptr, true,
                      (cudaStream_t)stream);
 }
 
@@ -426,7 +429,7 @@ int eb_policy_loss(eb_scorer_t* h, const eb_score_input_t* in, const eb_policy_t
   a.ent_coef = (float)p->entropy_coef;
   a.scale = p->scale;
   a.terms = terms;
-  return launch_rows(h, a, in->dtype, ebk::kModePolicy, true, d_logits != nullptr, false,
+  return launch_rows(h, a, in->dtype, ebk::kModePolicy, true, d_logits != nullptr,
                      (cudaStream_t)stream);
 }
 
@@ -451,8 +454,14 @@ int eb_preference_loss(eb_scorer_t* h, const eb_score_input_t* in, const eb_pref
   a.offsets = p->offsets;
   a.n_off = 2 * p->pairs;
   a.logprobs = logprobs ? logprobs : h->lp;
+  // the gradient's blocks, 32 KB of a row's aligned image each
+  constexpr int kBlock = ebk::kApplyThreads * ebk::kApplyGran * 16;
+  const int64_t image = (int64_t)in->V * (int64_t)elt_bytes(in->dtype) + 16;
+  int tiles = (int)((image + kBlock - 1) / kBlock);
+  if (d_logits && (int64_t)in->rows * tiles > 0x7fffffffll) return EB_ERR_OVERFLOW;
+  a.stats = d_logits ? h->stats : nullptr;
   if (in->rows > 0 &&
-      (rc = launch_rows(h, a, in->dtype, ebk::kModeScore, false, false, false, st)) != EB_OK)
+      (rc = launch_rows(h, a, in->dtype, ebk::kModeScore, false, false, st)) != EB_OK)
     return rc;
   if (p->pairs == 0) {
     if (cudaMemsetAsync(loss, 0, sizeof(float), st) != cudaSuccess) return EB_ERR_CUDA;
@@ -475,15 +484,24 @@ int eb_preference_loss(eb_scorer_t* h, const eb_score_input_t* in, const eb_pref
     q.g_lp = d_logits ? h->g : nullptr;
     q.counter = h->counter;
     q.status = h->status;
-    ebk::preference_kernel<<<p->pairs, ebk::kPrefThreads, 0, st>>>(q);
-    if (cudaGetLastError() != cudaSuccess) return EB_ERR_CUDA;
+    void* args[] = {&q};
+    if (!ebk::launch_dependent(reinterpret_cast<const void*>(&ebk::preference_kernel),
+                               dim3(p->pairs), dim3(ebk::kPrefThreads), 0, args, st))
+      return EB_ERR_CUDA;
   }
   if (!d_logits || in->rows == 0) return EB_OK;
   a.logprobs = nullptr;
   a.d_logits = d_logits;
   a.ldd = ldd;
   a.g_lp = h->g;
-  return launch_rows(h, a, in->dtype, ebk::kModeGrad, false, true, true, st);
+  void* args[] = {&a, &tiles};
+  const void* fn = in->dtype == EB_F32
+                       ? reinterpret_cast<const void*>(&ebk::score_apply_kernel<ebk::kScoreF32>)
+                       : reinterpret_cast<const void*>(&ebk::score_apply_kernel<ebk::kScoreBF16>);
+  return ebk::launch_dependent(fn, dim3((unsigned)in->rows * (unsigned)tiles),
+                               dim3(ebk::kApplyThreads), 0, args, st)
+             ? EB_OK
+             : EB_ERR_CUDA;
 }
 
 int eb_lmhead_logprobs(eb_scorer_t* h, const void* hidden, const void* weight, int32_t rows,

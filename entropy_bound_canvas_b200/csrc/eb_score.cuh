@@ -72,6 +72,7 @@ struct ScoreArgs {
   int n_off;
   float* logprobs;         // [rows] or null
   float* entropies;        // [rows] or null
+  float4* stats;           // [rows] or null: M, log2 S and its low part, 1 - p_a
   const float* g_lp;       // kModeGrad: upstream gradients
   const float* g_h;        // kModeGrad: or null
   const float* old_lp;     // kModePolicy
@@ -391,7 +392,7 @@ constexpr int kMaxCluster = 16;
 constexpr float kLazy = 2.0f;
 
 struct RingArgs {
-  int mode, reverse;
+  int mode;
   int log2C;     // CTAs per cluster: a power of two
   int stages;    // of the ring
   int ahead;     // two shares fit: the next row is folded before this one's gradient
@@ -762,7 +763,6 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
   cluster_sync_all();
 
   const RowRange range = row_range(p);
-  auto row_of = [&](int i) { return q.reverse ? p.rows - 1 - i : i; };
   auto fail = [&]() {
     atomicOr(p.status, kScoreTimeout);
     *(volatile int*)abort_flag = 1;
@@ -827,15 +827,15 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
     int token = -1;
     float weight = 1.f;
     if (i < p.rows) {
-      token = p.tokens[row_of(i)];
-      if (p.weights) weight = p.weights[row_of(i)];
+      token = p.tokens[i];
+      if (p.weights) weight = p.weights[i];
     }
     for (; i < p.rows && ok; i += ncl) {
-      const int row = row_of(i);
+      const int row = i;
       const bool on = range.live(row, token, weight);
       if (i + ncl < p.rows) {
-        token = p.tokens[row_of(i + ncl)];
-        if (p.weights) weight = p.weights[row_of(i + ncl)];
+        token = p.tokens[i + ncl];
+        if (p.weights) weight = p.weights[i + ncl];
       }
       if (!on) continue;
       const RowShare s = row_share<DT>(p.logits, p.ld, row, p.V, q.log2C, rank);
@@ -845,7 +845,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
       const int kept = min(n_st, q.keep);
       for (int k = 0; k < n_st && ok; ++k)
         copy_stage(s, img, s.g0 + k * kStageGran, s.g0 + min(s.n, (k + 1) * kStageGran),
-                   back && kept < n_st ? again : once);
+                   (back && kept < n_st) || p.stats ? again : once);
       if (back) {
         walk.turn();
         walk.step(kept);
@@ -881,13 +881,13 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
         }
       };
       int i = cid;
-      if (i < p.rows) fetch(row_of(i));
+      if (i < p.rows) fetch(i);
       for (; i < p.rows && ok; i += ncl) {
-        const int row = row_of(i);
+        const int row = i;
         const int a = token;
         const float wt = weight, y0 = x0, y1 = x1, y2 = x2;
         const float Trow = row_temp_ok(T) ? T : nan;
-        if (i + ncl < p.rows) fetch(row_of(i + ncl));
+        if (i + ncl < p.rows) fetch(i + ncl);
         if (!range.live(row, a, wt)) {
           if (first && lane == 0) {
             if (p.logprobs) p.logprobs[row] = 0.f;
@@ -954,6 +954,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
         if (first && lane == 0) {
           if (p.logprobs) p.logprobs[row] = r.lp;
           if (ENT && p.entropies) p.entropies[row] = r.H;
+          if (p.stats) p.stats[row] = make_float4(r.M, r.l2S, r.l2S_low, r.rest);
           const uint32_t bits = (bad ? kScoreBadToken : 0u) | (r.finite ? 0u : kScoreNonFinite);
           if (bits) atomicOr(p.status, bits);
           if (q.mode == kModePolicy) policy_add(p, o, r.H, wt, t);
@@ -1062,19 +1063,19 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
     int token = -1;
     float weight = 1.f, T = p.temp;
     if (i < p.rows) {
-      token = p.tokens[row_of(i)];
-      if (p.weights) weight = p.weights[row_of(i)];
-      if (p.temps) T = p.temps[row_of(i)];
+      token = p.tokens[i];
+      if (p.weights) weight = p.weights[i];
+      if (p.temps) T = p.temps[i];
     }
     for (; i < p.rows && ok; i += ncl) {
-      const int row = row_of(i);
+      const int row = i;
       const int a = token;
       const float wt = weight;
       const float c2 = log2e_over(row_temp_ok(T) ? T : nan);
       if (i + ncl < p.rows) {
-        token = p.tokens[row_of(i + ncl)];
-        if (p.weights) weight = p.weights[row_of(i + ncl)];
-        if (p.temps) T = p.temps[row_of(i + ncl)];
+        token = p.tokens[i + ncl];
+        if (p.weights) weight = p.weights[i + ncl];
+        if (p.temps) T = p.temps[i + ncl];
       }
       const RowShare sh = row_share<DT>(p.logits, p.ld, row, p.V, q.log2C, rank);
       if (!range.live(row, a, wt)) {
@@ -1203,7 +1204,7 @@ constexpr __host__ __device__ int short_bytes(int W) { return W * 32 * kShortGra
 
 template <int DT, bool ENT, bool GRAD, int W>
 __global__ void __launch_bounds__(kShortThreads, GRAD ? 6 : 8)
-    score_short_kernel(const ScoreArgs p, const int mode, const int reverse) {
+    score_short_kernel(const ScoreArgs p, const int mode) {
   constexpr int kB = ScoreType<DT>::kBytes, kPer = ScoreType<DT>::kPer16;
   constexpr int kRows = kShortThreads / 32 / W;  // per block
   constexpr int kT = W * 32;
@@ -1216,7 +1217,7 @@ __global__ void __launch_bounds__(kShortThreads, GRAD ? 6 : 8)
   int flip = 0;
   // W = 4: the block's warps share a row and meet at barriers
   for (int i = blockIdx.x * kRows + warp / W; i < p.rows; i += gridDim.x * kRows) {
-    const int row = reverse ? p.rows - 1 - i : i;
+    const int row = i;
     const int token = p.tokens[row];
     const float weight = p.weights ? p.weights[row] : 1.f;
     const RowShare sh = row_share<DT>(p.logits, p.ld, row, p.V, 0, 0);
@@ -1334,6 +1335,7 @@ __global__ void __launch_bounds__(kShortThreads, GRAD ? 6 : 8)
     if (tid == 0) {
       if (p.logprobs) p.logprobs[row] = r.lp;
       if (ENT && p.entropies) p.entropies[row] = r.H;
+      if (p.stats) p.stats[row] = make_float4(r.M, r.l2S, r.l2S_low, r.rest);
       const uint32_t bits = (bad ? kScoreBadToken : 0u) | (r.finite ? 0u : kScoreNonFinite);
       if (bits) atomicOr(p.status, bits);
     }
@@ -1357,6 +1359,89 @@ __global__ void __launch_bounds__(kShortThreads, GRAD ? 6 : 8)
   }
   if (mode == kModePolicy)
     policy_total<kShortThreads, kRows>(p, tid == 0 ? warp / W : -1, t, blockIdx.x, gridDim.x);
+}
+
+// ---------------------------------------------------------------------------
+// The gradient of g log p_a from the rows' statistics
+//
+// One read and one write: for a loss whose factor g needs every row's sums
+// first (the preference loss).  A block takes 32 KB of a row.  The rows go in
+// the opposite order of the pass that made the statistics, so that what that
+// pass read last is still in L2.
+// ---------------------------------------------------------------------------
+constexpr int kApplyThreads = 256, kApplyGran = 8;  // granules per thread
+
+template <int DT>
+__global__ void __launch_bounds__(kApplyThreads)
+    score_apply_kernel(const ScoreArgs p, const int tiles) {  // per row
+  constexpr int kB = ScoreType<DT>::kBytes, kPer = ScoreType<DT>::kPer16;
+  const int row = p.rows - 1 - (int)(blockIdx.x / (unsigned)tiles);
+  const int tile = tiles - 1 - (int)(blockIdx.x % (unsigned)tiles);
+  const RowShare sh = row_share<DT>(p.logits, p.ld, row, p.V, 0, 0);
+  const int g0 = tile * (kApplyThreads * kApplyGran) + (int)threadIdx.x;
+  const char* img = static_cast<const char*>(p.logits) + sh.base;
+  char* dz = static_cast<char*>(p.d_logits) + (int64_t)row * p.ldd * kB - sh.shift * kB;
+  const bool vec = ((uintptr_t)dz & 15u) == 0;
+  const int token = p.tokens[row];
+  float T = p.temps ? p.temps[row] : p.temp;
+  if (!row_temp_ok(T)) T = __int_as_float(0x7fc00000);
+  const Scale sc = row_scale(T);
+  const float iT = 1.f / T;
+  const RowRange range = row_range(p);
+  griddep_wait();  // the statistics and factors
+  const bool on = range.live(row, token, 1.f);
+  float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
+  float g = 0.f;
+  if (on) {
+    st = __ldcg(p.stats + row);
+    g = __ldcg(p.g_lp + row);
+  }
+  // p = 2^(d - l2S) 2^-l2S_low: the second factor goes into the coefficient
+  const float a0 = fmaf(-kLn2, st.z, 1.f) * (-iT * g), own = iT * g * st.w;
+  const uint64_t cc = pack2(sc.c2, sc.c2), nl = pack2(-st.y, -st.y), A0 = pack2(a0, a0);
+  const int at = token + sh.shift, ag = at / kPer, el = at & (kPer - 1);
+  uint4 w[kApplyGran];
+#pragma unroll
+  for (int j = 0; j < kApplyGran; ++j) {
+    const int gj = g0 + j * kApplyThreads;
+    if (on && gj >= sh.whole0 && gj < sh.whole1)
+      w[j] = __ldcs(reinterpret_cast<const uint4*>(img) + gj);
+  }
+#pragma unroll
+  for (int j = 0; j < kApplyGran; ++j) {
+    const int gj = g0 + j * kApplyThreads;
+    if (gj >= sh.n) break;
+    const bool whole = gj >= sh.whole0 && gj < sh.whole1;
+    float o[kPer];
+    if (!on) {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) o[k] = 0.f;
+    } else if (whole) {
+      granule_grad<DT, false>(w[j], st.x, cc, nl, A0, A0, o);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int v = gj * kPer + k - sh.shift;
+        o[k] = 0.f;
+        if (v >= 0 && v < p.V)
+          o[k] = a0 * ex2(fmaf(load_logit<DT>(img, (int64_t)gj * kPer + k) - st.x, sc.c2, -st.y));
+      }
+    }
+    if (on && gj == ag) {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (k == el) o[k] = own;
+    }
+    if (vec && whole) {
+      store_stream(reinterpret_cast<uint4*>(dz) + gj, granule_pack<DT>(o));
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int v = gj * kPer + k - sh.shift;
+        if (v >= 0 && v < p.V) store_grad<DT>(dz, (int64_t)gj * kPer + k, o[k]);
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -1400,6 +1485,7 @@ __global__ void __launch_bounds__(kPrefThreads) preference_kernel(const PrefArgs
   double S[2], share[2];
   int lo[2], hi[2];
   bool bad = false;
+  griddep_wait();  // the rows' log-probabilities
   for (int q = 0; q < 2; ++q) {
     const int s = k + q * p.pairs;
     const int a = p.offsets[s], b = p.offsets[s + 1];
