@@ -134,6 +134,12 @@ __device__ __forceinline__ void tc2_mma(uint32_t d_tmem, uint64_t adesc, uint64_
       : "memory");
 }
 
+// A bounded wait: one test, then the timed form.
+__device__ __forceinline__ bool lm_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                        const int* abort) {
+  return mbar_try_wait(bar, parity) || mbar_wait_timed(bar, parity, limit_ns, abort);
+}
+
 __device__ __forceinline__ float lm_temp(const LmScoreArgs& p, int row) {
   const float T = p.temps ? p.temps[row] : p.temp;
   return row_temp_ok(T) ? T : __int_as_float(0x7fc00000);
@@ -234,7 +240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLsThreads, 1)
       for (int t = 0; t < n_tiles && ok; ++t) {
         const int y = (nt_lo + t) * kLsBN + rank * kLsHalf;
         for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait(&empty[s], phase, p.wait_ns, abort_flag)) {
+          if (!lm_wait(&empty[s], phase, p.wait_ns, abort_flag)) {
             fail();
             ok = false;
             break;
@@ -264,14 +270,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLsThreads, 1)
         for (int kb = 0; kb < KB && ok; ++kb) {
           const int buf = used & 1, in_chunk = kb % kLsChunk;
           if (in_chunk == 0 && used >= 2) {
-            if (!mbar_wait(&acc_empty[buf], (uint32_t)(used / 2 - 1) & 1u, p.wait_ns,
+            if (!lm_wait(&acc_empty[buf], (uint32_t)(used / 2 - 1) & 1u, p.wait_ns,
                            abort_flag)) {
               ok = false;
               break;
             }
             tc_fence_after();
           }
-          if (!mbar_wait(&full[s], phase, p.wait_ns, abort_flag)) {
+          if (!lm_wait(&full[s], phase, p.wait_ns, abort_flag)) {
             ok = false;
             break;
           }
@@ -317,7 +323,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLsThreads, 1)
       for (int c = 0; c < chunks; ++c, ++used) {
         const int buf = used & 1;
         // a warp-uniform outcome: the TMEM loads below need the whole warp
-        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (uint32_t)(used / 2) & 1u,
+        if (!__all_sync(0xffffffffu, lm_wait(&acc_full[buf], (uint32_t)(used / 2) & 1u,
                                                p.wait_ns, abort_flag))) {
           ok = false;
           break;
@@ -485,7 +491,7 @@ __global__ void __launch_bounds__(FewShape<NH>::kThreads, 1)
       bool ok = true;
       for (int t = 0; t < n_tiles && ok; ++t) {
         for (int kb = 0; kb < KB; ++kb, ++issued) {
-          if (!mbar_wait(&empty[s], phase, p.wait_ns, abort_flag)) {
+          if (!lm_wait(&empty[s], phase, p.wait_ns, abort_flag)) {
             fail();
             ok = false;
             break;
@@ -516,14 +522,14 @@ __global__ void __launch_bounds__(FewShape<NH>::kThreads, 1)
         for (int kb = 0; kb < KB && ok; ++kb) {
           const int buf = used & 1, in_chunk = kb % kLsChunk;
           if (in_chunk == 0 && used >= 2) {
-            if (!mbar_wait(&acc_empty[buf], (uint32_t)(used / 2 - 1) & 1u, p.wait_ns,
+            if (!lm_wait(&acc_empty[buf], (uint32_t)(used / 2 - 1) & 1u, p.wait_ns,
                            abort_flag)) {
               ok = false;
               break;
             }
             tc_fence_after();
           }
-          if (!mbar_wait(&full[s], phase, p.wait_ns, abort_flag)) {
+          if (!lm_wait(&full[s], phase, p.wait_ns, abort_flag)) {
             ok = false;
             break;
           }
@@ -567,7 +573,7 @@ __global__ void __launch_bounds__(FewShape<NH>::kThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c, ++used) {
         const int buf = used & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (uint32_t)(used / 2) & 1u,
+        if (!__all_sync(0xffffffffu, lm_wait(&acc_full[buf], (uint32_t)(used / 2) & 1u,
                                                p.wait_ns, abort_flag))) {
           ok = false;
           break;

@@ -741,7 +741,7 @@ const char* eb_strerror(int code) {
   }
 }
 
-int eb_version(void) { return 200; }
+int eb_version(void) { return 210; }
 
 }  // extern "C"
 

@@ -6,7 +6,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -60,9 +59,23 @@ struct DeviceInfo {
   int rc = EB_ERR_CUDA;
   int sms = 0;
   size_t optin = 0;
-  std::atomic<int> clusters[kVariants][kMaxLog2C + 1];  // that fit at once, plus 1; 0: not asked
+  int clusters[kVariants][kMaxLog2C + 1];  // ring clusters of 2^c CTAs that fit at once
 };
 DeviceInfo g_info[kMaxDevices];
+
+void ring_config(cudaLaunchConfig_t& lc, cudaLaunchAttribute& attr, int clusters, int log2C,
+                 cudaStream_t st) {
+  std::memset(&lc, 0, sizeof(lc));
+  lc.gridDim = dim3((unsigned)clusters << log2C);
+  lc.blockDim = dim3(ebk::kRingThreads);
+  lc.dynamicSmemBytes = ebk::ring_layout(kRingStages).total;
+  lc.stream = st;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 1u << log2C;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  lc.attrs = &attr;
+  lc.numAttrs = 1;
+}
 
 void info_setup(DeviceInfo& d, int device) {
   int sms = 0, optin = 0, major = 0;
@@ -109,6 +122,22 @@ void info_setup(DeviceInfo& d, int device) {
       d.rc = EB_ERR_CUDA;
       return;
     }
+  for (int v = 0; v < kVariants; ++v)
+    for (int c = 0; c <= kMaxLog2C; ++c) {
+      cudaLaunchConfig_t lc;
+      cudaLaunchAttribute attr;
+      ring_config(lc, attr, 1, c, nullptr);
+      int most = 0;
+      if (cudaOccupancyMaxActiveClusters(&most, kRing[v], &lc) != cudaSuccess) {
+        cudaGetLastError();
+        most = 0;  // this size is not used
+      }
+      d.clusters[v][c] = std::max(0, std::min(most, kMaxGrid));
+    }
+  if (d.clusters[0][0] < 1) {
+    d.rc = EB_ERR_CUDA;
+    return;
+  }
   d.sms = sms;
   d.optin = (size_t)optin;
   d.rc = EB_OK;
@@ -176,39 +205,6 @@ void fill_args(const eb_scorer* h, const eb_score_input_t* in, ScoreArgs& a) {
   a.wait_ns = h->wait_ns;
 }
 
-void ring_config(cudaLaunchConfig_t& lc, cudaLaunchAttribute& attr, int clusters, int log2C,
-                 cudaStream_t st) {
-  std::memset(&lc, 0, sizeof(lc));
-  lc.gridDim = dim3((unsigned)clusters << log2C);
-  lc.blockDim = dim3(ebk::kRingThreads);
-  lc.dynamicSmemBytes = ebk::ring_layout(kRingStages).total;
-  lc.stream = st;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 1u << log2C;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  lc.attrs = &attr;
-  lc.numAttrs = 1;
-}
-
-// Clusters of 2^log2C ring CTAs that fit the device at once (the current
-// one), asked once per variant and size; 0: none.
-int ring_clusters(int device, int variant, int log2C) {
-  std::atomic<int>& cached = g_info[device].clusters[variant][log2C];
-  const int known = cached.load(std::memory_order_relaxed);
-  if (known > 0) return known - 1;
-  cudaLaunchConfig_t lc;
-  cudaLaunchAttribute attr;
-  ring_config(lc, attr, 1, log2C, nullptr);
-  int most = 0;
-  if (cudaOccupancyMaxActiveClusters(&most, kRing[variant], &lc) != cudaSuccess) {
-    cudaGetLastError();
-    most = 0;
-  }
-  most = std::max(0, std::min(most, kMaxGrid));
-  cached.store(most + 1, std::memory_order_relaxed);
-  return most;
-}
-
 int share_stages(int64_t row_bytes, int log2C) {
   // the aligned image of a row spans up to one granule more than its bytes
   const int64_t G = (row_bytes + 15) / 16 + 1;
@@ -233,7 +229,7 @@ int ring_log2C(const eb_scorer* h, int variant, bool f32, bool grad, int64_t row
   int best = 0;
   double best_t = 0.0;
   for (int c = 0; c <= kMaxLog2C; ++c) {
-    const int n = ring_clusters(h->device, variant, c);
+    const int n = g_info[h->device].clusters[variant][c];
     if (n < 1) break;
     const double share = kb / (1 << c), fixed = (grad ? 1.4 : 1.1) + 0.1 * c;
     // the part of a share that the ring does not keep is copied again, from
@@ -283,7 +279,7 @@ int launch_rows(const eb_scorer* h, const ScoreArgs& a, int dtype, int mode, boo
                : EB_ERR_CUDA;
   }
   const int c = ring_log2C(h, v, dtype == EB_F32, grad, a.rows, row_bytes);
-  const int most = ring_clusters(h->device, v, c);
+  const int most = g_info[h->device].clusters[v][c];
   if (most < 1) return EB_ERR_CUDA;
   ebk::RingArgs q;
   q.mode = mode;

@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
   // only where that fails.  The outcome is the whole warp's.
   auto wait = [&](uint64_t* bar, uint32_t ph) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, ph))) return true;
-    return (bool)__all_sync(0xffffffffu, mbar_wait(bar, ph, p.wait_ns, abort_flag));
+    return (bool)__all_sync(0xffffffffu, mbar_wait_timed(bar, ph, p.wait_ns, abort_flag));
   };
   bool ok = true;
   const float nan = __int_as_float(0x7fc00000);
@@ -977,7 +977,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
     // The token's place in this CTA's share: this thread's granule (counted
     // along its own granules, -1: another thread's) and element.
     auto place = [&](const RowShare& sh, int token, int& el) {
-      const int at = token + sh.shift, ag = at / kPer - sh.g0;
+      const int at = min(token, p.V) + sh.shift, ag = at / kPer - sh.g0;
       el = at & (kPer - 1);
       return token < p.V && ag >= 0 && ag < sh.n && (ag & (kT - 1)) == tid ? ag / kT : -1;
     };
@@ -1294,7 +1294,7 @@ __global__ void __launch_bounds__(kShortThreads, GRAD ? 6 : 8)
     const Scale sc = row_scale(T);
     const float c2 = sc.c2;
     const bool bad = token >= p.V;
-    const int at = token + sh.shift, ag = at / kPer, el = at & (kPer - 1);
+    const int at = min(token, p.V) + sh.shift, ag = at / kPer, el = at & (kPer - 1);
     const int mine = !bad && ag % kT == tid ? ag / kT : -1;
     ThreadSums s;
     s.m = -FLT_MAX;
@@ -1399,7 +1399,7 @@ __global__ void __launch_bounds__(kApplyThreads)
   // p = 2^(d - l2S) 2^-l2S_low: the second factor goes into the coefficient
   const float a0 = fmaf(-kLn2, st.z, 1.f) * (-iT * g), own = iT * g * st.w;
   const uint64_t cc = pack2(sc.c2, sc.c2), nl = pack2(-st.y, -st.y), A0 = pack2(a0, a0);
-  const int at = token + sh.shift, ag = at / kPer, el = at & (kPer - 1);
+  const int at = min(token, p.V) + sh.shift, ag = at / kPer, el = at & (kPer - 1);
   uint4 w[kApplyGran];
 #pragma unroll
   for (int j = 0; j < kApplyGran; ++j) {

@@ -561,6 +561,85 @@ def test_two_scorers_on_two_streams(E):
     b.close()
 
 
+@pytest.mark.parametrize("dtype,V", [(F32, 1000003), (BF16, 3000001)])
+def test_rows_longer_than_the_rings(scorer, dtype, V):
+    """A row of several megabytes: its shares are copied twice on every cluster."""
+    rows = 3
+    z, tokens, _ = R.make_logits(rows, V, dtype, 9, DEV, shift=1)
+    g, h = randn(rows, 1), randn(rows, 2)
+    check_scores(scorer.token_logprobs(z, tokens, temperature=0.9), z, 0.9, tokens)
+    for gh in (h, None):
+        d = scorer.token_logprobs_backward(z, tokens, g, gh, temperature=0.9)
+        R.check_gradient(d, *R.gradient(z, 0.9, tokens, g, gh), dtype)
+    z[1, 5:V - 3] = -math.inf
+    tokens[1] = V - 1
+    d = scorer.token_logprobs_backward(z, tokens, g, h, temperature=0.9)
+    R.check_gradient(d, *R.gradient(z, 0.9, tokens, g, h), dtype)
+    assert scorer.status() == 0
+
+
+@pytest.mark.parametrize("V", [1000, 40000])
+def test_offsets_past_32_bits(scorer, V):
+    """Rows 1.2e9 elements apart: the last one starts 2.4e9 elements in."""
+    rows, ld = 3, 1200000007
+    buf = torch.empty(2 * ld + V + 8, dtype=BF16, device=DEV)
+    z = buf.as_strided((rows, V), (ld, 1), 0)
+    src, tokens, _ = R.make_logits(rows, V, BF16, 3, DEV)
+    for i in range(rows):
+        z[i].copy_(src[i])
+    near = scorer.token_logprobs(src, tokens, temperature=0.7)
+    far = scorer.token_logprobs(z, tokens, temperature=0.7)
+    assert (near.logprobs - far.logprobs).abs().max() < 1e-5
+    g = randn(rows, 1)
+    want = scorer.token_logprobs_backward(src, tokens, g, g, temperature=0.7)
+    got = scorer.token_logprobs_backward(z, tokens, g, g, temperature=0.7, out=z)
+    assert got is z
+    ref, tol = R.gradient(src, 0.7, tokens, g, g)
+    R.check_gradient(torch.stack([z[i] for i in range(rows)]), ref, tol, BF16)
+    R.check_gradient(want, ref, tol, BF16)
+    off = torch.tensor([0, 2, 3], dtype=torch.int32, device=DEV)
+    for i in range(rows):
+        z[i].copy_(src[i])
+    a = scorer.preference_loss(src, tokens, off)
+    b = scorer.preference_loss(z, tokens, off, out=z)
+    assert abs(float(a.loss) - float(b.loss)) < 1e-5
+    assert (a.d_logits.float() - torch.stack([z[i] for i in range(rows)]).float()).abs().max() < 1e-3
+
+
+def test_a_wait_that_runs_out_is_reported(E):
+    """With a limit of 1 ns the first wait for a copy gives up: the status word
+    says so, no result passes for a good one, and the next calls are right."""
+    sc = E.EBScorer(512, device=DEV)
+    z, tokens, old, ref, adv = policy_inputs(sc, 300, 20000, BF16, 3)
+    h = torch.randn((300, 256), generator=torch.Generator().manual_seed(1)).to(BF16).to(DEV)
+    w = torch.randn((5000, 256), generator=torch.Generator().manual_seed(2)).to(BF16).to(DEV)
+    t = tokens % 5000
+
+    def calls():
+        p = sc.policy_loss(z, tokens, old, adv, ref_logprobs=ref, temperature=0.8, **POLICY)
+        return [p.terms, p.logprobs, p.d_logits, sc.lmhead_logprobs(h, w, t).logprobs,
+                sc.lmhead_logprobs(h[:20], w, t[:20]).logprobs]
+
+    want = calls()
+    assert sc.status() == 0
+    sc.set_wait_limit(1)
+    terms = sc.policy_loss(z, tokens, old, adv, ref_logprobs=ref, temperature=0.8,
+                           **POLICY).terms
+    assert sc.status(clear=True) & E.STATUS_TIMEOUT
+    assert torch.isnan(terms).all()
+    lp = sc.lmhead_logprobs(h, w, t).logprobs
+    assert sc.status(clear=True) & E.STATUS_TIMEOUT
+    assert torch.isnan(lp).any()
+    lp = sc.lmhead_logprobs(h[:20], w, t[:20]).logprobs
+    assert sc.status(clear=True) & E.STATUS_TIMEOUT
+    assert torch.isnan(lp).all()
+    sc.set_wait_limit(0)
+    got = calls()
+    assert sc.status() == 0
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    sc.close()
+
+
 def test_refusals(E, scorer):
     z = torch.zeros((4, 64), device=DEV)
     t = torch.zeros(4, dtype=torch.int32, device=DEV)
