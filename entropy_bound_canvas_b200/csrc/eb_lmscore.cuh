@@ -156,7 +156,8 @@ __device__ __forceinline__ void lm_fold(RowSums& s, const uint64_t (&z)[kLsHalf 
     unpack2(z[i], a, b);
     hi = fmaxf(hi, fmaxf(a, b));
   }
-  if ((hi - s.m) * c2 > kLazy) s = row_sums_join(s, RowSums{hi, 0.f, 0.f}, c2);
+  // moved only by 2^2: see kMuch on what that costs
+  if ((hi - s.m) * c2 > 2.f) s = row_sums_join(s, RowSums{hi, 0.f, 0.f}, c2);
   const uint64_t nm = pack2(-s.m, -s.m), cc = pack2(c2, c2);
   uint64_t R[2] = {}, Q[2] = {};
 #pragma unroll

@@ -149,7 +149,7 @@ __device__ __forceinline__ RowSums row_sums_shuffle(RowSums s, int mask, float c
 }
 
 struct RowResult {
-  float M;             // maximum over every logit (or near it, see kLazy)
+  float M;             // maximum over every logit (or near it, see kMuch)
   float l2S, l2S_low;  // log2 S, and what its rounding left
   float lp, lp_low;    // log p_a (nats), and what its rounding left
   float H;             // entropy (nats)
@@ -385,11 +385,12 @@ constexpr int kStageGran = kRingWarps * 32 * kStageIter;
 constexpr int kStageBytes = kStageGran * 16;
 constexpr int kMaxCluster = 16;
 
-// A thread moves its reference to a new maximum only when that exceeds it by
-// 2^kLazy: a row that one logit dominates still has that logit as its
-// reference (any other is over 2^kLazy below it), and the others' sums are as
-// exact relative to a nearby value.
-constexpr float kLazy = 2.0f;
+// A thread's reference is the maximum of what it folds first.  It moves only
+// when a fold's sum relative to it exceeds kMuch (or is not finite), so that
+// the common fold looks for no maximum.  The sums are as exact relative to a
+// nearby value; a logit that dominates its row is over kMuch times any other's
+// term, so it becomes the reference, and its own term is exactly 1.
+constexpr float kMuch = 64.0f;
 
 struct RingArgs {
   int mode;
@@ -618,11 +619,11 @@ __device__ __forceinline__ void granule_sums(const uint4 (&w)[N], float m, float
 }
 
 // The thread's sums moved to the reference of N granules' maximum, where that
-// is 2^kLazy above theirs or more.
+// is above theirs.
 template <int DT, bool ENT, int N>
 __device__ __forceinline__ void raise(ThreadSums& s, const uint4 (&w)[N], float c2) {
   const float hi = granule_max<DT, N>(w);
-  if (!((hi - s.m) * c2 > kLazy)) return;  // the empty reference is -FLT_MAX
+  if (!(hi > s.m)) return;  // the empty reference is -FLT_MAX
   const float d = fmaxf((s.m - hi) * c2, -kDeep), f = ex2(d);
   const uint64_t f2 = pack2(f, f), d2 = pack2(d, d);
 #pragma unroll
@@ -633,14 +634,20 @@ __device__ __forceinline__ void raise(ThreadSums& s, const uint4 (&w)[N], float 
   s.m = hi;
 }
 
-// Folds N granules into a thread's sums.  `drop`: the element that is left out
-// (counted through the N granules), or -1; its value goes to `za`.
+// Folds N granules into a thread's sums.  `fresh`: the row's first.  `drop`: the
+// element that is left out (counted through the N granules), or -1; its value
+// goes to `za`.
 template <int DT, bool ENT, int N>
-__device__ __forceinline__ void fold(ThreadSums& s, uint4 (&w)[N], int drop, float c2, float& za) {
+__device__ __forceinline__ void fold(ThreadSums& s, uint4 (&w)[N], bool fresh, int drop, float c2,
+                                     float& za) {
   if (drop >= 0) za = granule_drop<DT, N>(w, drop);
-  raise<DT, ENT, N>(s, w, c2);
+  if (fresh) raise<DT, ENT, N>(s, w, c2);
   uint64_t R[2], Q[2];
   granule_sums<DT, ENT, N>(w, s.m, c2, R, Q);
+  if (!(pair_sum(R) <= kMuch)) {
+    raise<DT, ENT, N>(s, w, c2);
+    granule_sums<DT, ENT, N>(w, s.m, c2, R, Q);
+  }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     s.R[k] = add2(s.R[k], R[k]);
@@ -1122,14 +1129,15 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
           uint4 w[kIter];
 #pragma unroll
           for (int j = 0; j < kIter; ++j) w[j] = st[j * kT];
-          fold<DT, ENT, kIter>(s, w, drop, c2, za);
+          fold<DT, ENT, kIter>(s, w, k == 0, drop, c2, za);
         } else {
           // past the share's end: what is left, one granule at a time
 #pragma unroll 1
           for (int j = 0; j < kIter - 1 && j * kT + tid < n; ++j) {
             uint4 w[1] = {st[j * kT]};
-            fold<DT, ENT, 1>(s, w, drop >= j * kPer && drop < (j + 1) * kPer ? drop - j * kPer : -1,
-                             c2, za);
+            fold<DT, ENT, 1>(s, w, k == 0 && j == 0,
+                             drop >= j * kPer && drop < (j + 1) * kPer ? drop - j * kPer : -1, c2,
+                             za);
           }
         }
         if (k < n_st - stay) {
@@ -1307,7 +1315,8 @@ __global__ void __launch_bounds__(kShortThreads, GRAD ? 6 : 8)
 #pragma unroll
       for (int k = 0; k < kShortChunk; ++k) v[k] = w[c][k];
       const int j = mine - c * kShortChunk;
-      fold<DT, ENT, kShortChunk>(s, v, j >= 0 && j < kShortChunk ? j * kPer + el : -1, c2, za);
+      fold<DT, ENT, kShortChunk>(s, v, c == 0, j >= 0 && j < kShortChunk ? j * kPer + el : -1, c2,
+                                 za);
     }
     RowSums all = warp_join(RowSums{s.m, pair_sum(s.R), ENT ? pair_sum(s.Q) : 0.f}, c2);
     const unsigned holder = __ballot_sync(0xffffffffu, mine >= 0);
