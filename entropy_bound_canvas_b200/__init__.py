@@ -516,7 +516,10 @@ class EBScorer:
         _check(_lib().eb_scorer_init(C.byref(h), self.max_rows, self.device.index),
                "eb_scorer_init")
         self._h = h
-        self._f32 = torch.empty((0,), dtype=torch.float32, device=self.device)
+        self._f32 = torch.empty((1,), dtype=torch.float32, device=self.device)
+        self._shapes = {}
+        self._i32, self._bf16, self._Tensor = torch.int32, torch.bfloat16, torch.Tensor
+        self._like, self._dense = torch.empty_like, torch.contiguous_format
         # the stream's handle without a Stream object, where torch offers it
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._raw_stream = raw or (lambda i: torch.cuda.current_stream(i).cuda_stream)
@@ -529,68 +532,71 @@ class EBScorer:
         """Address of a contiguous tensor of n values (None: a null pointer)."""
         if t is None:
             return None
-        if not isinstance(t, _torch().Tensor):
+        if not isinstance(t, self._Tensor):
             raise TypeError(f"{name} must be a torch tensor")
+        if t.dtype is dtype and t.device == self.device and t.numel() == n and t.is_contiguous():
+            return t.data_ptr()
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, scorer is on {self.device}")
         if t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.numel() != n or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous and hold {n} values, "
-                             f"got {tuple(t.shape)}")
-        return t.data_ptr()
+        raise ValueError(f"{name} must be contiguous and hold {n} values, got {tuple(t.shape)}")
 
     def _matrix(self, t, name):
-        """(2-D view [rows, V], elements between rows) of logits or a gradient."""
-        torch = _torch()
-        if not isinstance(t, torch.Tensor):
+        """(address, rows, V, elements between rows) of logits or a gradient."""
+        if not isinstance(t, self._Tensor):
             raise TypeError(f"{name} must be a torch tensor")
-        if t.dtype != torch.float32 and t.dtype != torch.bfloat16:
+        if t.dtype is not self._f32.dtype and t.dtype is not self._bf16:
             raise TypeError(f"{name} must be float32 or bfloat16")
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, scorer is on {self.device}")
-        if t.dim() < 2:
-            raise ValueError(f"{name} must be [rows, V]")
-        if t.dim() > 2:
+        if t.dim() != 2:
+            if t.dim() < 2:
+                raise ValueError(f"{name} must be [rows, V]")
             try:
                 t = t.view(-1, t.shape[-1])
             except RuntimeError:
                 raise ValueError(f"{name}: the rows must lie at one stride") from None
         rows, V = t.shape
-        if V > 1 and t.stride(1) != 1:
+        ld, step = t.stride()
+        if V > 1 and step != 1:
             raise ValueError(f"{name} must have unit stride along V")
-        ld = t.stride(0) if rows > 1 else V
-        if ld < V:
+        if rows <= 1:
+            ld = V
+        elif ld < V:
             raise ValueError(f"{name}: rows overlap")
-        return t, ld
+        return t.data_ptr(), rows, V, ld
 
     def _input(self, logits, tokens, temperature):
-        torch = _torch()
-        z, ld = self._matrix(logits, "logits")
-        rows, V = z.shape
-        s = ScoreInput()
-        s.logits = z.data_ptr()
-        s.dtype = F32 if z.dtype == torch.float32 else BF16
-        s.rows, s.V, s.ld = rows, V, ld
-        s.tokens = self._vector(tokens, rows, torch.int32, "tokens")
-        if isinstance(temperature, torch.Tensor):
-            s.temperatures = self._vector(temperature, rows, torch.float32, "temperature")
-        else:
-            s.temperature = float(temperature)
-        return s
+        ptr, rows, V, ld = self._matrix(logits, "logits")
+        dtype = F32 if logits.dtype is self._f32.dtype else BF16
+        tok = self._vector(tokens, rows, self._i32, "tokens")
+        if isinstance(temperature, self._Tensor):
+            return ScoreInput(ptr, dtype, rows, V, ld, tok,
+                              self._vector(temperature, rows, self._f32.dtype, "temperature"), 0.0)
+        return ScoreInput(ptr, dtype, rows, V, ld, tok, None, temperature)
 
-    def _gradient(self, logits, out):
+    def _gradient(self, logits, s, out):
         """(gradient tensor shaped as the logits, its address, its row stride)."""
-        torch = _torch()
         if out is None:
-            out = torch.empty_like(logits, memory_format=torch.contiguous_format)
-        elif out.shape != logits.shape or out.dtype != logits.dtype:
+            out = self._like(logits, memory_format=self._dense)
+            return out, out.data_ptr(), s.V
+        if not isinstance(out, self._Tensor):
+            raise TypeError("out must be a torch tensor")
+        if out.shape != logits.shape or out.dtype != logits.dtype:
             raise ValueError("out must have the logits' shape and type")
-        d, ldd = self._matrix(out, "out")
-        return out, d.data_ptr(), ldd
+        ptr, _, _, ldd = self._matrix(out, "out")
+        return out, ptr, ldd
 
     def _new(self, n):
-        return self._f32.new_empty((n,))
+        """n fp32 values (empty_like of a kept shape without memory of its own:
+        the cheapest of torch's allocations)."""
+        shape = self._shapes.get(n)
+        if shape is None:
+            if len(self._shapes) >= 256:
+                self._shapes.clear()
+            shape = self._shapes[n] = self._f32.expand(n)
+        return self._like(shape, memory_format=self._dense)
 
     # -- calls ------------------------------------------------------------------
     def token_logprobs(self, logits, tokens, temperature=1.0, entropies: bool = True):
@@ -606,13 +612,13 @@ class EBScorer:
     def token_logprobs_backward(self, logits, tokens, d_logprobs, d_entropies=None,
                                 temperature=1.0, out=None):
         """The gradient for the logits from those of token_logprobs' results."""
-        torch = _torch()
         s = self._input(logits, tokens, temperature)
-        out, ptr, ldd = self._gradient(logits, out)
+        n, f32 = s.rows, self._f32.dtype
+        out, ptr, ldd = self._gradient(logits, s, out)
         _check(_lib().eb_token_logprobs_backward(
-            self._h, C.byref(s), self._vector(d_logprobs, s.rows, torch.float32, "d_logprobs"),
-            self._vector(d_entropies, s.rows, torch.float32, "d_entropies"), ptr, ldd,
-            self._stream()), "eb_token_logprobs_backward")
+            self._h, C.byref(s), self._vector(d_logprobs, n, f32, "d_logprobs"),
+            self._vector(d_entropies, n, f32, "d_entropies"), ptr, ldd, self._stream()),
+            "eb_token_logprobs_backward")
         return out
 
     def policy_loss(self, logits, tokens, old_logprobs, advantages, ref_logprobs=None,
@@ -620,15 +626,14 @@ class EBScorer:
                     entropy_coef=0.0, scale=1.0, grad: bool = True, out=None):
         """Clipped policy loss with a KL term and an entropy bonus, and its
         gradient for the logits (grad=False: the loss alone)."""
-        f32 = _torch().float32
         s = self._input(logits, tokens, temperature)
-        n = s.rows
+        n, f32 = s.rows, self._f32.dtype
         p = Policy(self._vector(old_logprobs, n, f32, "old_logprobs"),
                    self._vector(advantages, n, f32, "advantages"),
                    self._vector(ref_logprobs, n, f32, "ref_logprobs"),
                    self._vector(weights, n, f32, "weights"), clip_low, clip_high, kl_coef,
                    entropy_coef, scale)
-        d, ptr, ldd = self._gradient(logits, out) if grad else (None, None, 0)
+        d, ptr, ldd = self._gradient(logits, s, out) if grad else (None, None, 0)
         terms, lp, h = self._new(5), self._new(n), self._new(n)
         _check(_lib().eb_policy_loss(self._h, C.byref(s), C.byref(p), terms.data_ptr(),
                                      lp.data_ptr(), h.data_ptr(), ptr, ldd, self._stream()),
@@ -642,18 +647,18 @@ class EBScorer:
         logits.  offsets [2 pairs + 1] int32 (device): sequence s is the rows
         offsets[s]..offsets[s+1], the chosen sequences first, then the
         rejected ones; ref_logprobs [2 pairs] a reference model's sums."""
-        torch = _torch()
         s = self._input(logits, tokens, temperature)
-        if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 \
+        n, f32 = s.rows, self._f32.dtype
+        if not isinstance(offsets, self._Tensor) or offsets.dim() != 1 \
                 or offsets.numel() % 2 != 1:
             raise ValueError("offsets must be a 1-D tensor of 2 * pairs + 1 values")
         pairs = offsets.numel() // 2
-        p = Preference(self._vector(offsets, 2 * pairs + 1, torch.int32, "offsets"), pairs,
-                       self._vector(ref_logprobs, 2 * pairs, torch.float32, "ref_logprobs"),
+        p = Preference(self._vector(offsets, 2 * pairs + 1, self._i32, "offsets"), pairs,
+                       self._vector(ref_logprobs, 2 * pairs, f32, "ref_logprobs"),
                        beta, label_smoothing, margin, int(average), scale)
-        d, ptr, ldd = self._gradient(logits, out) if grad else (None, None, 0)
+        d, ptr, ldd = self._gradient(logits, s, out) if grad else (None, None, 0)
         loss, losses, seq, lp = (self._new(1), self._new(pairs), self._new(2 * pairs),
-                                 self._new(s.rows))
+                                 self._new(n))
         _check(_lib().eb_preference_loss(self._h, C.byref(s), C.byref(p), loss.data_ptr(),
                                          losses.data_ptr(), seq.data_ptr(), lp.data_ptr(), ptr,
                                          ldd, self._stream()), "eb_preference_loss")
@@ -662,11 +667,10 @@ class EBScorer:
     def lmhead_logprobs(self, hidden, weight, tokens, temperature=1.0, entropies: bool = True):
         """token_logprobs on the logits hidden @ weight^T (bf16 [rows, d] or
         [B, L, d], and [V, d]) without forming them in memory."""
-        torch = _torch()
         for t, n in ((hidden, "hidden"), (weight, "weight")):
-            if not isinstance(t, torch.Tensor):
+            if not isinstance(t, self._Tensor):
                 raise TypeError(f"{n} must be a torch tensor")
-            if t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != self.device:
+            if t.dtype != self._bf16 or not t.is_contiguous() or t.device != self.device:
                 raise ValueError(f"{n} must be a contiguous bf16 tensor on {self.device}")
         if hidden.dim() < 2 or weight.dim() != 2 or weight.shape[1] != hidden.shape[-1]:
             raise ValueError("hidden must be [rows, d] and weight [V, d]")
@@ -674,11 +678,11 @@ class EBScorer:
         rows = hidden.numel() // d if d else 0
         lp = self._new(rows)
         h = self._new(rows) if entropies else None
-        tensor = isinstance(temperature, torch.Tensor)
+        tensor = isinstance(temperature, self._Tensor)
         _check(_lib().eb_lmhead_logprobs(
             self._h, hidden.data_ptr(), weight.data_ptr(), rows, V, d,
-            self._vector(tokens, rows, torch.int32, "tokens"),
-            self._vector(temperature, rows, torch.float32, "temperature") if tensor else None,
+            self._vector(tokens, rows, self._i32, "tokens"),
+            self._vector(temperature, rows, self._f32.dtype, "temperature") if tensor else None,
             1.0 if tensor else float(temperature), lp.data_ptr(),
             h.data_ptr() if entropies else None, self._stream()), "eb_lmhead_logprobs")
         return TokenScores(lp, h)

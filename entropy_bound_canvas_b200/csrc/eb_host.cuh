@@ -12,12 +12,21 @@
 
 namespace ebk {
 
-// Restores the caller's current device on scope exit.
+// Makes a device current, and the caller's again on scope exit.
 struct DeviceGuard {
-  int prev = -1;
+  int prev = -1;  // to restore; -1: it was current already
   bool ok = false;
   explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) ok = true;
+    int now = -1;
+    if (cudaGetDevice(&now) != cudaSuccess) return;
+    if (now == dev) {
+      ok = true;
+      return;
+    }
+    if (cudaSetDevice(dev) == cudaSuccess) {
+      prev = now;
+      ok = true;
+    }
   }
   ~DeviceGuard() {
     if (prev >= 0) cudaSetDevice(prev);
