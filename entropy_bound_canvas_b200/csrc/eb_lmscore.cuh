@@ -16,11 +16,14 @@
 // The tensor cores add each K = 16 step's products to the accumulator with
 // truncation: about 2^-26 of the sum lost per step, always toward zero (1.6e-8
 // measured; over the 160 steps of d = 2560 a logit of 10 was 2.6e-5 low, five
-// times what fp32 summation loses).  So an accumulator takes 1024 elements of
-// K at most, and the pieces are added in registers, rounded to nearest (512
-// cost 6 % of the time of 2048 rows, 1024 less than 1 %).
+// times what fp32 summation loses).  So an accumulator takes 512 elements of
+// K at most, and the pieces are added in registers, rounded to nearest (1 % of
+// the time of 2048 rows against 1024 elements, for half the error).
 //
-// Up to 64 rows that product would be mostly padding: lmfew_kernel turns it
+// 65 to 128 rows would leave half of a pair's product padding: there each CTA
+// works alone on its own vocabulary range, with M = 128.
+//
+// Up to 64 rows that product would be mostly padding too: lmfew_kernel turns it
 // around (W's rows on the 128 TMEM lanes, h's as 32 or 64 columns), so that
 // only the reading of W is left.
 //
@@ -35,15 +38,22 @@
 namespace ebk {
 
 constexpr int kLsRows = 128;          // rows per CTA
-constexpr int kLsBM = 2 * kLsRows;    // rows per pair
 constexpr int kLsBN = 256, kLsBK = 64;
-constexpr int kLsHalf = kLsBN / 2;    // rows of W a CTA loads, columns a thread holds
-constexpr int kLsStages = 6;
-constexpr int kLsChunk = 16;          // stages of one accumulator: 1024 elements of K
+constexpr int kLsHalf = kLsBN / 2;    // rows of W in one copy, columns a thread holds
+constexpr int kLsChunk = 8;           // stages of one accumulator: 512 elements of K
 constexpr int kLsEpiWarps = 8;
 constexpr int kLsThreads = (2 + kLsEpiWarps) * 32;
 constexpr uint32_t kLsABytes = kLsRows * kLsBK * 2, kLsBBytes = kLsHalf * kLsBK * 2;
-constexpr uint32_t kLsStageBytes = kLsABytes + kLsBBytes;
+template <bool PAIR>
+struct LsShape {
+  static constexpr int kCtas = PAIR ? 2 : 1;
+  static constexpr int kBM = kCtas * kLsRows;     // rows of a tile
+  static constexpr int kCopies = PAIR ? 1 : 2;    // of W's tile, by this CTA
+  static constexpr int kStages = PAIR ? 6 : 4;
+  static constexpr uint32_t kStage = kLsABytes + kCopies * kLsBBytes;
+  static constexpr uint32_t kBars = kStages * kStage,
+                            kSmem = kBars + 8 * (2 * kStages + 5) + 16 + 1024;
+};
 constexpr uint32_t kLsTmemCols = 2 * kLsBN;
 
 using LmSums = RowSums;
@@ -63,29 +73,21 @@ struct LmScoreArgs {
   float* entropies;
 };
 
-// Vocabulary ranges per row tile: one pair per two SMs over all tiles.
+// Vocabulary ranges per row tile: one CTA per SM over all tiles.
+template <bool PAIR>
 inline int lm_score_split(int sms, int64_t rows, int64_t V) {
-  const int64_t n_mt = (rows + kLsBM - 1) / kLsBM, n_nt = (V + kLsBN - 1) / kLsBN;
-  const int64_t fit = sms / 2 / n_mt;
+  using S = LsShape<PAIR>;
+  const int64_t n_mt = (rows + S::kBM - 1) / S::kBM, n_nt = (V + kLsBN - 1) / kLsBN;
+  const int64_t fit = sms / S::kCtas / n_mt;
   const int64_t s = n_nt < fit ? n_nt : fit;
   return s < 1 ? 1 : (int)s;
 }
 
-// Most (half range, row) records of any call of up to max_rows rows: sms / 2
-// / n_mt ranges of n_mt 256-row tiles, two halves each, or one range.
+// Most (half range, row) records of any call of up to max_rows rows: ranges x
+// tile rows is at most sms x 128, two halves each; or one range.
 inline size_t lm_score_slots(int sms, int64_t max_rows) {
-  const size_t wide = (size_t)sms * (size_t)kLsBM, tall = 2 * (size_t)max_rows;
+  const size_t wide = 2 * (size_t)sms * (size_t)kLsRows, tall = 2 * (size_t)max_rows;
   return tall > wide ? tall : wide;
-}
-
-struct LmScoreLayout {
-  uint32_t bars, total;
-};
-__host__ __device__ constexpr LmScoreLayout lm_score_layout() {
-  LmScoreLayout y{};
-  y.bars = kLsStages * kLsStageBytes;
-  y.total = y.bars + 8u * (2 * kLsStages + 5) + 16u + 1024u;
-  return y;
 }
 
 // -- the cta_group::2 forms ------------------------------------------------------
@@ -178,46 +180,53 @@ __device__ __forceinline__ void lm_fold(RowSums& s, const uint64_t (&z)[kLsHalf 
   s.Q += pair_sum(Q);
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLsThreads, 1)
+template <bool PAIR>
+__global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kLsThreads, 1)
     lmscore_kernel(const __grid_constant__ CUtensorMap tm_h,
                    const __grid_constant__ CUtensorMap tm_w, const LmScoreArgs p) {
+  using S = LsShape<PAIR>;
   extern __shared__ unsigned char ls_smem_raw[];
   // the same offset in both CTAs: the MMA's descriptors and the commits name it
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(ls_smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lm_score_layout().bars);
-  uint64_t* empty = full + kLsStages;
-  uint64_t* acc_full = empty + kLsStages;  // [2]
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBars);
+  uint64_t* empty = full + S::kStages;
+  uint64_t* acc_full = empty + S::kStages;  // [2]
   uint64_t* acc_empty = acc_full + 2;      // [2]
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = (int)cluster_rank();
-  const int pair = blockIdx.x >> 1;
+  const int rank = PAIR ? (int)cluster_rank() : 0;
+  const int pair = blockIdx.x / S::kCtas;
   const int n_nt = (p.V + kLsBN - 1) / kLsBN;
   const int mt = pair / p.n_split, ns = pair % p.n_split;
   const int nt_lo = (int)((long long)ns * n_nt / p.n_split);
   const int nt_hi = (int)((long long)(ns + 1) * n_nt / p.n_split);
   const int n_tiles = nt_hi - nt_lo;
   const int KB = (p.d + kLsBK - 1) / kLsBK;
-  const int row0 = mt * kLsBM + rank * kLsRows;
+  const int row0 = mt * S::kBM + rank * kLsRows;
 
   if (tid == 0) {
-    for (int s = 0; s < kLsStages; ++s) {
+    for (int s = 0; s < S::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 2 * kLsEpiWarps);
+      mbar_init(&acc_empty[b], S::kCtas * kLsEpiWarps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 0) tc2_alloc(tmem_slot, kLsTmemCols);
+  if (warp == 0) {
+    if (PAIR)
+      tc2_alloc(tmem_slot, kLsTmemCols);
+    else
+      tc_alloc(tmem_slot, kLsTmemCols);
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
@@ -234,7 +243,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLsThreads, 1)
     if (lane == 0) {
       const uint64_t keep = evict_last_policy();  // h: every vocabulary tile reads it again
       // W: read once, or by every row tile at about the same time
-      const uint64_t wpol = p.rows > kLsBM ? keep : evict_first_policy();
+      const uint64_t wpol = p.rows > S::kBM ? keep : evict_first_policy();
       int s = 0;
       uint32_t phase = 1u;  // an empty stage's first wait passes at once
       bool ok = true;
@@ -246,13 +255,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLsThreads, 1)
             ok = false;
             break;
           }
-          // the first CTA's barrier counts both CTAs' bytes
-          const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kLsStageBytes);
-          unsigned char* dst = smem + s * kLsStageBytes;
-          tma_load_pair(dst, &tm_h, kb * kLsBK, row0, bar, keep);
-          tma_load_pair(dst + kLsABytes, &tm_w, kb * kLsBK, y, bar, wpol);
-          if (++s == kLsStages) {
+          unsigned char* dst = smem + s * S::kStage;
+          if (PAIR) {
+            // the first CTA's barrier counts both CTAs' bytes
+            const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::kStage);
+            tma_load_pair(dst, &tm_h, kb * kLsBK, row0, bar, keep);
+            tma_load_pair(dst + kLsABytes, &tm_w, kb * kLsBK, y, bar, wpol);
+          } else {
+            mbar_arrive_expect_tx(&full[s], S::kStage);
+            tma_load_2d(dst, &tm_h, kb * kLsBK, row0, &full[s], keep);
+            tma_load_2d(dst + kLsABytes, &tm_w, kb * kLsBK, y, &full[s], wpol);
+            tma_load_2d(dst + kLsABytes + kLsBBytes, &tm_w, kb * kLsBK, y + kLsHalf, &full[s],
+                        wpol);
+          }
+          if (++s == S::kStages) {
             s = 0;
             phase ^= 1u;
           }
@@ -262,8 +279,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLsThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------- MMA issuer
     if (rank == 0 && lane == 0) {
-      constexpr uint32_t idesc = lm_idesc(kLsBM, kLsBN);
+      constexpr uint32_t idesc = lm_idesc(S::kBM, kLsBN);
       const uint32_t base = smem_u32(smem);
+      auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t i, uint32_t acc) {
+        if (PAIR)
+          tc2_mma(d, a, b, i, acc);
+        else
+          tc_mma(d, a, b, i, acc);
+      };
+      auto commit = [](uint64_t* bar) {
+        if (PAIR)
+          tc2_commit(bar);
+        else
+          tc_commit(bar);
+      };
       int s = 0, used = 0;  // stage; accumulators filled
       uint32_t phase = 0u;
       bool ok = true;
@@ -283,25 +312,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLsThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t a = base + (uint32_t)s * kLsStageBytes, b = a + kLsABytes;
+          const uint32_t a = base + (uint32_t)s * S::kStage, b = a + kLsABytes;
 #pragma unroll
           for (int k = 0; k < kLsBK / 16; ++k)
-            tc2_mma(tmem + (uint32_t)(buf * kLsBN), sw128_desc(a + k * 32u), sw128_desc(b + k * 32u),
-                    idesc, (in_chunk | k) != 0 ? 1u : 0u);
-          tc2_commit(&empty[s]);  // in both CTAs: the stage has been read
-          if (++s == kLsStages) {
+            mma(tmem + (uint32_t)(buf * kLsBN), sw128_desc(a + k * 32u), sw128_desc(b + k * 32u),
+                idesc, (in_chunk | k) != 0 ? 1u : 0u);
+          commit(&empty[s]);  // in both CTAs: the stage has been read
+          if (++s == S::kStages) {
             s = 0;
             phase ^= 1u;
           }
           if (in_chunk == kLsChunk - 1 || kb == KB - 1) {
-            tc2_commit(&acc_full[buf]);
+            commit(&acc_full[buf]);
             ++used;
           }
         }
       }
       if (!ok) fail();
       // every MMA issued has completed before TMEM is released
-      tc2_commit(drain);
+      commit(drain);
       mbar_wait(drain, 0u, kDrainLimitNs);
     }
   } else {
@@ -382,16 +411,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLsThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  // after a cut-short pass copies may still be on their way into either CTA:
-  // they land well within this pause
+  // after a cut-short pass copies may still be on their way into either CTA's
+  // memory: they land well within this pause
   if (*(volatile int*)abort_flag) __nanosleep(200000);
   __syncwarp();
   cluster_sync_all();
   tc_fence_after();
   if (warp == 0) {
     __syncwarp();
-    tc2_dealloc(tmem, kLsTmemCols);
-    tc2_relinquish();
+    if (PAIR) {
+      tc2_dealloc(tmem, kLsTmemCols);
+      tc2_relinquish();
+    } else {
+      tc_dealloc(tmem, kLsTmemCols);
+      tc_relinquish();
+    }
   }
 }
 

@@ -91,12 +91,13 @@ void info_setup(DeviceInfo& d, int device) {
     d.rc = EB_ERR_UNSUPPORTED;
     return;
   }
-  const int lm_smem[3] = {(int)ebk::lm_score_layout().total, (int)ebk::FewShape<1>::kSmem,
-                          (int)ebk::FewShape<2>::kSmem};
-  const void* lm_fn[3] = {reinterpret_cast<const void*>(&ebk::lmscore_kernel),
+  const int lm_smem[4] = {(int)ebk::LsShape<true>::kSmem, (int)ebk::LsShape<false>::kSmem,
+                          (int)ebk::FewShape<1>::kSmem, (int)ebk::FewShape<2>::kSmem};
+  const void* lm_fn[4] = {reinterpret_cast<const void*>(&ebk::lmscore_kernel<true>),
+                          reinterpret_cast<const void*>(&ebk::lmscore_kernel<false>),
                           reinterpret_cast<const void*>(&ebk::lmfew_kernel<1>),
                           reinterpret_cast<const void*>(&ebk::lmfew_kernel<2>)};
-  for (int k = 0; k < 3; ++k) {
+  for (int k = 0; k < 4; ++k) {
     if (lm_smem[k] > optin) {
       d.rc = EB_ERR_UNSUPPORTED;
       return;
@@ -528,12 +529,13 @@ int eb_lmhead_logprobs(eb_scorer_t* h, const void* hidden, const void* weight, i
   p.status = h->status;
   p.logprobs = logprobs;
   p.entropies = entropies;
-  const bool few = rows <= ebk::kLfRows;
+  const bool few = rows <= ebk::kLfRows, pair = rows > ebk::kLsRows;
   if (few) {
     p.n_split = std::min(h->sms, (V + 127) / 128);
     p.n_rec = p.n_split;
   } else {
-    p.n_split = ebk::lm_score_split(h->sms, rows, V);
+    p.n_split = pair ? ebk::lm_score_split<true>(h->sms, rows, V)
+                     : ebk::lm_score_split<false>(h->sms, rows, V);
     p.n_rec = 2 * p.n_split;
   }
   if ((size_t)p.n_rec * (size_t)rows > h->lm_slots) return EB_ERR_OVERFLOW;
@@ -543,10 +545,13 @@ int eb_lmhead_logprobs(eb_scorer_t* h, const void* hidden, const void* weight, i
                       !few ? ebk::kLsRows : wide ? 64 : 32) ||
       !ebk::make_tmap(&tw, weight, (uint64_t)d, (uint64_t)V, ebk::kLsBK, 128))
     return EB_ERR_CUDA;
-  if (!few) {
-    const int n_mt = (rows + ebk::kLsBM - 1) / ebk::kLsBM;
-    ebk::lmscore_kernel<<<2 * n_mt * p.n_split, ebk::kLsThreads, ebk::lm_score_layout().total,
-                          st>>>(th, tw, p);
+  if (pair) {
+    using S = ebk::LsShape<true>;
+    const int n_mt = (rows + S::kBM - 1) / S::kBM;
+    ebk::lmscore_kernel<true><<<2 * n_mt * p.n_split, ebk::kLsThreads, S::kSmem, st>>>(th, tw, p);
+  } else if (!few) {
+    ebk::lmscore_kernel<false><<<p.n_split, ebk::kLsThreads, ebk::LsShape<false>::kSmem, st>>>(
+        th, tw, p);
   } else if (wide) {
     ebk::lmfew_kernel<2><<<p.n_split, ebk::FewShape<2>::kThreads, ebk::FewShape<2>::kSmem, st>>>(
         th, tw, p);
