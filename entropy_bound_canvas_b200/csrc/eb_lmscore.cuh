@@ -20,8 +20,8 @@
 // K at most, and the pieces are added in registers, rounded to nearest (1 % of
 // the time of 2048 rows against 1024 elements, for half the error).
 //
-// 65 to 128 rows would leave half of a pair's product padding: there each CTA
-// works alone on its own vocabulary range, with M = 128.
+// Where a pair's product would be half padding (65 to 128 rows, and small odd
+// numbers of 128-row tiles) each CTA works alone, with M = 128.
 //
 // Up to 64 rows that product would be mostly padding too: lmfew_kernel turns it
 // around (W's rows on the 128 TMEM lanes, h's as 32 or 64 columns), so that

@@ -436,7 +436,8 @@ def test_bad_offsets_are_reported_and_stay_inside(scorer):
                                       (128, 513, 200), (129, 4096, 64), (300, 5000, 264),
                                       (257, 2047, 2560), (600, 32003, 128), (2, 70001, 64),
                                       (32, 1001, 1032), (33, 128, 64), (50, 3000, 2056),
-                                      (64, 40001, 96), (65, 300, 1096), (128, 40001, 2560), (100, 255, 520)])
+                                      (64, 40001, 96), (65, 300, 1096), (128, 40001, 2560), (100, 255, 520),
+                                      (383, 3001, 600), (1300, 2100, 72), (1500, 700, 136)])
 def test_lmhead_scores(scorer, rows, V, d):
     """Codes over 8: the products' fp32 sums are exact, so the logits are the
     64-bit ones and only the softmax rounds."""
