@@ -531,6 +531,13 @@ __device__ __forceinline__ Granule<DT> granule_minus(const uint4& w, float m) {
   return g;
 }
 
+// A granule of -inf: no part of any sum.
+template <int DT>
+__device__ __forceinline__ uint4 nothing() {
+  const uint32_t x = DT == kScoreF32 ? 0xff800000u : 0xff80ff80u;
+  return make_uint4(x, x, x, x);
+}
+
 // Largest element of N granules (NaN is passed over: it shows in the sums).
 template <int DT, int N>
 __device__ __forceinline__ float granule_max(const uint4 (&w)[N]) {
@@ -1023,21 +1030,28 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
         const uint4* st = reinterpret_cast<const uint4*>(ring + (size_t)at * kStageBytes) + tid;
         const int n = sh.n - st_no * kStageGran, first = st_no * kIter;
         const int g = sh.g0 + st_no * kStageGran + tid;
-        // a stage of whole granules without the token
-        const bool plain = (kIter - 1) * kT + tid < n && dz_vec &&
-                           (unsigned)(mine - first) >= (unsigned)kIter && g >= sh.whole0 &&
-                           g + (kIter - 1) * kT < sh.whole1;
-        if (plain) {
-          uint4* out = reinterpret_cast<uint4*>(dz) + g;
+        // this thread's granules of the stage: whole ones without the token?
+        const int many = min(kIter, (n - tid + kT - 1) / kT);
+        const bool plain = dz_vec && (unsigned)(mine - first) >= (unsigned)kIter &&
+                           g >= sh.whole0 && g + (many - 1) * kT < sh.whole1;
+        uint4* out = reinterpret_cast<uint4*>(dz) + g;
+        if (plain && many == kIter) {
 #pragma unroll
           for (int j = 0; j < kIter; ++j) {
             float o[kPer];
             granule_grad<DT, ENT>(st[j * kT], r.M, cc, nl, A0, A1, o);
             store_stream(out + j * kT, granule_pack<DT>(o));
           }
+        } else if (plain) {
+#pragma unroll 1
+          for (int j = 0; j < many; ++j) {
+            float o[kPer];
+            granule_grad<DT, ENT>(st[j * kT], r.M, cc, nl, A0, A1, o);
+            store_stream(out + j * kT, granule_pack<DT>(o));
+          }
         } else {
 #pragma unroll 1
-          for (int j = 0; j < kIter && j * kT + tid < n; ++j) {
+          for (int j = 0; j < many; ++j) {
             const int gj = g + j * kT;
             float o[kPer];
             granule_grad<DT, ENT>(st[j * kT], r.M, cc, nl, A0, A1, o);
@@ -1130,15 +1144,11 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
 #pragma unroll
           for (int j = 0; j < kIter; ++j) w[j] = st[j * kT];
           fold<DT, ENT, kIter>(s, w, k == 0, drop, c2, za);
-        } else {
-          // past the share's end: what is left, one granule at a time
-#pragma unroll 1
-          for (int j = 0; j < kIter - 1 && j * kT + tid < n; ++j) {
-            uint4 w[1] = {st[j * kT]};
-            fold<DT, ENT, 1>(s, w, k == 0 && j == 0,
-                             drop >= j * kPer && drop < (j + 1) * kPer ? drop - j * kPer : -1, c2,
-                             za);
-          }
+        } else if (tid < n) {  // nothing past the share's end
+          uint4 w[kIter];
+#pragma unroll
+          for (int j = 0; j < kIter; ++j) w[j] = j * kT + tid < n ? st[j * kT] : nothing<DT>();
+          fold<DT, ENT, kIter>(s, w, k == 0, drop, c2, za);
         }
         if (k < n_st - stay) {
           __syncwarp();
@@ -1264,8 +1274,7 @@ __global__ void __launch_bounds__(kShortThreads, GRAD ? 6 : 8)
 #pragma unroll
     for (int c = 0; c < kShortGran; ++c) {
       const int g = c * kT + tid;
-      uint4 x = kB == 4 ? make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u)
-                        : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+      uint4 x = nothing<DT>();
       if (g < sh.n) {
         if (g >= sh.whole0 && g < sh.whole1) {
           x = reinterpret_cast<const uint4*>(img)[g];
