@@ -216,6 +216,54 @@ def test_row_temperatures_and_ignored_rows(scorer, dtype, rows, V):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,V", [
+    (4096, 300), (2500, 2003), (1900, 4001),   # short rows, several to a block
+    (900, 9001), (1000, 20011),                # several rows to a cluster, two shares in the ring
+    (650, 70001), (310, 131072)])              # shares longer than the ring, copied twice
+def test_many_rows_in_turn(scorer, dtype, rows, V):
+    """More rows than are in flight, a fifth of them ignored: every row against
+    the 64-bit form, in blocks."""
+    z, tokens, _ = R.make_logits(rows, V, dtype, rows + V, DEV, banned=V // 50)
+    tokens = tokens.clone()
+    tokens[torch.rand(rows, generator=torch.Generator().manual_seed(2)) < 0.2] = -1
+    T = 0.4 + 0.8 * torch.rand(rows, generator=torch.Generator().manual_seed(5)).to(DEV)
+    g, h = randn(rows, 1), randn(rows, 2)
+    r = scorer.token_logprobs(z, tokens, temperature=T)
+    both = scorer.token_logprobs_backward(z, tokens, g, h, temperature=T)
+    one = scorer.token_logprobs_backward(z, tokens, g, None, temperature=T)
+    _, _, old, ref, adv = policy_inputs(scorer, rows, 8, F32, 5)
+    lp, H = r
+    old = (lp + 0.2 * randn(rows, 3)).contiguous()
+    p = scorer.policy_loss(z, tokens, old, adv, temperature=T, scale=0.01,
+                           **dict(POLICY, kl_coef=0.0))
+    for lo in range(0, rows, 128):
+        at = slice(lo, lo + 128)
+        zb, tb, Tb = z[at], tokens[at], T[at]
+        check_scores(type(r)(lp[at], H[at]), zb, Tb, tb)
+        check_scores(type(r)(p.logprobs[at], p.entropies[at]), zb, Tb, tb)
+        R.check_gradient(both[at], *R.gradient(zb, Tb, tb, g[at], h[at]), dtype)
+        R.check_gradient(one[at], *R.gradient(zb, Tb, tb, g[at], None), dtype)
+    # the policy's gradient is that of its own factors
+    ratio = torch.exp(lp.double() - old.double())
+    free = -adv.double() * ratio
+    cut = -adv.double() * ratio.clamp(0.8, 1.28) > free
+    gp = torch.where((tokens >= 0) & ~cut, 0.01 * free, 0.0).float()
+    hp = torch.full_like(gp, -0.01 * POLICY["entropy_coef"])
+    d = scorer.token_logprobs_backward(z, tokens, gp, hp, temperature=T)
+    # Apart by the gradients' own roundings, and by the factor's: the ratio here
+    # comes from log p_a as written (half a step of its fp32 value, and what
+    # two summation orders leave), and the factor is rounded a few times; an
+    # element is at most factor / T.
+    tl = torch.cat([R.logprob_tol(z[lo:lo + 128], T[lo:lo + 128], tokens[lo:lo + 128])[0]
+                    for lo in range(0, rows, 128)])
+    rel = torch.where(tokens >= 0, R.U * lp.double().abs() + 2 * tl + 16 * R.U, 0.0)
+    bound = (gp.double().abs() * rel / T.double())[:, None] \
+        + 4 * R.half_step(dtype) * d.double().abs() + 2.0 ** -120
+    assert ((p.d_logits.double() - d.double()).abs() <= bound).all()
+    assert scorer.status() == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_in_place_gradient_equals_the_separate_one(scorer, dtype):
     for rows, V in ((5, 1000), (40, 32003), (3, 262144)):
         z, tokens, _ = R.make_logits(rows, V, dtype, V, DEV)
