@@ -413,7 +413,7 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kLsThread
   __syncthreads();
   // after a cut-short pass copies may still be on their way into either CTA's
   // memory: they land well within this pause
-  if (*(volatile int*)abort_flag) __nanosleep(200000);
+  if (*(volatile int*)abort_flag) pause_ns(200000);
   __syncwarp();
   cluster_sync_all();
   tc_fence_after();

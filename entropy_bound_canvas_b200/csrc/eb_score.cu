@@ -51,14 +51,13 @@ const void* const kShort[2][kVariants] = {
      short_fn<ebk::kScoreBF16, false, false, 4>(), short_fn<ebk::kScoreBF16, false, true, 4>(),
      short_fn<ebk::kScoreBF16, true, false, 4>(), short_fn<ebk::kScoreBF16, true, true, 4>()}};
 
-constexpr int kRingStages = 6;  // two CTAs of 96 KB rings share an SM
+using ebk::kRingStages;
 constexpr int kMaxLog2C = 4;
 
 struct DeviceInfo {
   std::once_flag once;
   int rc = EB_ERR_CUDA;
   int sms = 0;
-  size_t optin = 0;
   int clusters[kVariants][kMaxLog2C + 1];  // ring clusters of 2^c CTAs that fit at once
 };
 DeviceInfo g_info[kMaxDevices];
@@ -68,7 +67,7 @@ void ring_config(cudaLaunchConfig_t& lc, cudaLaunchAttribute& attr, int clusters
   std::memset(&lc, 0, sizeof(lc));
   lc.gridDim = dim3((unsigned)clusters << log2C);
   lc.blockDim = dim3(ebk::kRingThreads);
-  lc.dynamicSmemBytes = ebk::ring_layout(kRingStages).total;
+  lc.dynamicSmemBytes = ebk::ring_layout().total;
   lc.stream = st;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = 1u << log2C;
@@ -109,7 +108,7 @@ void info_setup(DeviceInfo& d, int device) {
       return;
     }
   }
-  const uint32_t ring_smem = ebk::ring_layout(kRingStages).total;
+  const uint32_t ring_smem = ebk::ring_layout().total;
   if (ring_smem > (uint32_t)optin) {
     d.rc = EB_ERR_UNSUPPORTED;
     return;
@@ -140,7 +139,6 @@ void info_setup(DeviceInfo& d, int device) {
     return;
   }
   d.sms = sms;
-  d.optin = (size_t)optin;
   d.rc = EB_OK;
 }
 
@@ -150,7 +148,6 @@ struct eb_scorer {
   int device = 0;
   int max_rows = 0;
   int sms = 0;
-  size_t optin = 0;
   uint64_t wait_ns = ebk::kWaitLimitNs;
   void* ws = nullptr;
   size_t ws_bytes = 0;
@@ -169,6 +166,9 @@ namespace {
 
 size_t elt_bytes(int dtype) { return dtype == EB_F32 ? 4 : 2; }
 
+// Positive and finite, as the fp32 that the kernels use.
+bool temperature_ok(double t) { return (float)t > 0.f && std::isfinite((float)t); }
+
 // Sizes, types and pointers every call over logits shares.
 int check_input(const eb_scorer* h, const eb_score_input_t* in) {
   if (!h || !in) return EB_ERR_INVALID_ARG;
@@ -177,8 +177,7 @@ int check_input(const eb_scorer* h, const eb_score_input_t* in) {
   if (in->rows > h->max_rows || in->V > (1 << 30) || in->ld > (1ll << 40)) return EB_ERR_OVERFLOW;
   if (in->rows > 0 && (!in->logits || !in->tokens)) return EB_ERR_INVALID_ARG;
   if ((uintptr_t)in->logits % elt_bytes(in->dtype) != 0) return EB_ERR_INVALID_ARG;
-  if (!in->temperatures && !(in->temperature > 0.0 && std::isfinite(in->temperature)))
-    return EB_ERR_INVALID_ARG;
+  if (!in->temperatures && !temperature_ok(in->temperature)) return EB_ERR_INVALID_ARG;
   return EB_OK;
 }
 
@@ -214,17 +213,20 @@ int share_stages(int64_t row_bytes, int log2C) {
 }
 
 // The cluster size of a ring launch.  A row on 2^c CTAs costs a CTA its share
-// of the row at the CTA's rate, and about a microsecond more for the exchange;
+// of the row at the CTA's rate, and one to two microseconds for the exchange;
 // rows go in waves of the clusters that fit.  More CTAs per row shorten the
 // last, partly filled wave and (with a gradient, whose second look at a row
 // should find it in L2) keep fewer rows in flight; fewer pay the exchange less
 // often.  The rates are what one CTA was measured to take, in KB/us: alone on
-// its SM, and with every SM holding two.  Measured both ways, 262144 bf16:
-// one row, forward, 22.6 us on one CTA and 5.5 on 16; 600 rows, with gradient,
-// 161 us on one CTA each, 134 on two, 170 on eight.
+// its SM, and with every SM holding two; the other constants were fitted to
+// 22 shapes of 100 to 2048 rows on one to eight CTAs each, where the size
+// taken is within 2 % of the best on average and 8 % at most.  262144 bf16:
+// one row, forward, 22.6 us on one CTA and 5.5 on 16; 2048 rows with their
+// gradient 478 us on one CTA each, 400 on two, 436 on four, 528 on eight;
+// 2048 rows of 16000: 46 on one, 55 on two.
 int ring_log2C(const eb_scorer* h, int variant, bool f32, bool grad, int64_t rows,
                int64_t row_bytes) {
-  const double alone = (grad ? 13.0 : 26.0) * (f32 ? 1.4 : 1.0);
+  const double alone = (grad ? 12.0 : 26.0) * (f32 ? 1.4 : 1.0);
   const double full = (grad ? 9.3 : 18.0) * (f32 ? 1.25 : 1.0);
   const double kb = (double)row_bytes / 1024.0;
   int best = 0;
@@ -232,16 +234,17 @@ int ring_log2C(const eb_scorer* h, int variant, bool f32, bool grad, int64_t row
   for (int c = 0; c <= kMaxLog2C; ++c) {
     const int n = g_info[h->device].clusters[variant][c];
     if (n < 1) break;
-    const double share = kb / (1 << c), fixed = (grad ? 1.4 : 1.1) + 0.1 * c;
+    const double share = kb / (1 << c), fixed = grad ? 1.2 + 0.3 * c : 1.1 + 0.1 * c;
     // the part of a share that the ring does not keep is copied again, from
-    // L2, or from HBM where more rows are in flight than L2 keeps
-    const double flight = (double)std::min<int64_t>(n, rows) * kb / 1024.0;
+    // L2, or from HBM where the rows in flight ask for more than L2 keeps
+    double again = 1.0;
     const int stages = share_stages(row_bytes, c);
-    const double over = std::min(1.0, std::max(0.0, (flight - 40.0) / 100.0));
-    const double again =
-        grad && stages > kRingStages
-            ? 1.0 + (1.0 - (double)kRingStages / stages) * (0.3 + 0.3 * over)
-            : 1.0;
+    if (grad && stages > kRingStages) {
+      const double part = 1.0 - (double)kRingStages / stages;
+      const double asked = (double)std::min<int64_t>(n, rows) * kb / 1024.0 * part;
+      const double over = std::min(1.0, std::max(0.0, (asked - 40.0) / 60.0));
+      again = 1.0 + part * (0.1 + 0.5 * over);
+    }
     const int64_t waves = rows / n, left = rows - waves * n;
     double t = (double)waves * (fixed + share / full * again);
     if (left > 0) {
@@ -285,9 +288,7 @@ int launch_rows(const eb_scorer* h, const ScoreArgs& a, int dtype, int mode, boo
   ebk::RingArgs q;
   q.mode = mode;
   q.log2C = c;
-  q.stages = kRingStages;
   q.ahead = 2 * share_stages(row_bytes, c) <= kRingStages;
-  q.keep = kRingStages;
   cudaLaunchConfig_t lc;
   cudaLaunchAttribute attr;
   ring_config(lc, attr, std::max(1, std::min(a.rows, most)), c, st);
@@ -319,7 +320,6 @@ int eb_scorer_init(eb_scorer_t** out, int32_t max_rows, int device) {
   h->device = device;
   h->max_rows = max_rows;
   h->sms = d.sms;
-  h->optin = d.optin;
   h->lm_slots = ebk::lm_score_slots(d.sms, max_rows);
   size_t off = 0;
   const size_t o_status = off;
@@ -402,8 +402,8 @@ int eb_policy_loss(eb_scorer_t* h, const eb_score_input_t* in, const eb_policy_t
   if (rc != EB_OK) return rc;
   if (!p || !terms) return EB_ERR_INVALID_ARG;
   if (!(p->clip_low >= 0.0 && p->clip_low <= 1.0) || !(p->clip_high >= 0.0) ||
-      !std::isfinite(p->clip_high) || !std::isfinite(p->kl_coef) ||
-      !std::isfinite(p->entropy_coef) || !std::isfinite(p->scale))
+      !std::isfinite((float)p->clip_high) || !std::isfinite((float)p->kl_coef) ||
+      !std::isfinite((float)p->entropy_coef) || !std::isfinite(p->scale))
     return EB_ERR_INVALID_ARG;
   if (p->kl_coef != 0.0 && !p->ref_logprobs && in->rows > 0) return EB_ERR_INVALID_ARG;
   if (in->rows > 0 && (!p->old_logprobs || !p->advantages)) return EB_ERR_INVALID_ARG;
@@ -507,8 +507,7 @@ int eb_lmhead_logprobs(eb_scorer_t* h, const void* hidden, const void* weight, i
   if (!h || rows < 0 || V < 1 || d < 1) return EB_ERR_INVALID_ARG;
   if (d % 8 != 0) return EB_ERR_UNSUPPORTED;
   if (rows > h->max_rows || V > (1 << 30) || d > (1 << 20)) return EB_ERR_OVERFLOW;
-  if (!temperatures && !(temperature > 0.0 && std::isfinite(temperature)))
-    return EB_ERR_INVALID_ARG;
+  if (!temperatures && !temperature_ok(temperature)) return EB_ERR_INVALID_ARG;
   if (rows == 0) return EB_OK;
   if (!hidden || !weight || !tokens || !logprobs) return EB_ERR_INVALID_ARG;
   if ((uintptr_t)hidden % 16 != 0 || (uintptr_t)weight % 16 != 0) return EB_ERR_INVALID_ARG;

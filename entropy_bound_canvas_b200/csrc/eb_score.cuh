@@ -140,14 +140,6 @@ __device__ __forceinline__ RowSums row_sums_join(RowSums a, RowSums b, float c2)
                  fmaf(fa, fmaf(da, a.R, a.Q), fb * fmaf(db, b.R, b.Q))};
 }
 
-__device__ __forceinline__ RowSums row_sums_shuffle(RowSums s, int mask, float c2) {
-  RowSums o;
-  o.m = __shfl_xor_sync(0xffffffffu, s.m, mask);
-  o.R = __shfl_xor_sync(0xffffffffu, s.R, mask);
-  o.Q = __shfl_xor_sync(0xffffffffu, s.Q, mask);
-  return row_sums_join(s, o, c2);
-}
-
 struct RowResult {
   float M;             // maximum over every logit (or near it, see kMuch)
   float l2S, l2S_low;  // log2 S, and what its rounding left
@@ -383,6 +375,7 @@ constexpr int kRingCtas = 2;   // per SM
 constexpr int kStageIter = 4;  // granules of a stage per consumer thread
 constexpr int kStageGran = kRingWarps * 32 * kStageIter;
 constexpr int kStageBytes = kStageGran * 16;
+constexpr int kRingStages = 6;  // two CTAs of 96 KB rings share an SM
 constexpr int kMaxCluster = 16;
 
 // A thread's reference is the maximum of what it folds first.  It moves only
@@ -395,22 +388,20 @@ constexpr float kMuch = 64.0f;
 struct RingArgs {
   int mode;
   int log2C;     // CTAs per cluster: a power of two
-  int stages;    // of the ring
   int ahead;     // two shares fit: the next row is folded before this one's gradient
-  int keep;      // not ahead: the share's last stages kept for the gradient
 };
 
 // The ring's slots in their order of use, the same for the producer and the
 // consumers, each slot with the parity of its next wait.
 struct RingWalk {
-  int slot, dir, stages;
+  int slot, dir;
   uint32_t parity;  // by slot
   __device__ __forceinline__ uint32_t phase() const { return parity >> slot & 1u; }
   __device__ __forceinline__ void used() { parity ^= 1u << slot; }
   __device__ __forceinline__ void step(int n = 1) {
     slot += dir * n;
-    if (slot >= stages) slot -= stages;
-    if (slot < 0) slot += stages;
+    if (slot >= kRingStages) slot -= kRingStages;
+    if (slot < 0) slot += kRingStages;
   }
   // The next slot is the one used last.
   __device__ __forceinline__ void turn() {
@@ -423,12 +414,12 @@ constexpr int kSlots = 4;  // rows between a slot's uses, see the kernel
 struct RingLayout {
   uint32_t part, grad, bars, flag, total;
 };
-__host__ __device__ constexpr RingLayout ring_layout(int stages) {
+__host__ __device__ constexpr RingLayout ring_layout() {
   RingLayout y{};
-  y.part = (uint32_t)(stages * kStageBytes);
+  y.part = (uint32_t)(kRingStages * kStageBytes);
   y.grad = y.part + (uint32_t)(kSlots * kMaxCluster * kRingWarps * 16);
   y.bars = y.grad + kSlots * 32u;
-  y.flag = y.bars + (2u * (uint32_t)stages + 2u * kSlots) * 8u;
+  y.flag = y.bars + (2u * (uint32_t)kRingStages + 2u * kSlots) * 8u;
   y.total = y.flag + 16u;
   return y;
 }
@@ -488,6 +479,11 @@ __device__ __forceinline__ void st_async4(uint32_t addr, float a, float b, float
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
+}
+// At least this long.
+__device__ __forceinline__ void pause_ns(uint64_t ns) {
+  const uint64_t t0 = global_ns();
+  while (global_ns() - t0 < ns) __nanosleep(1000);
 }
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -739,7 +735,6 @@ __device__ __forceinline__ RowShare row_share(const void* buf, int64_t ld, int r
   return s;
 }
 
-
 template <int DT, bool ENT, bool GRAD>
 __global__ void __launch_bounds__(kRingThreads, kRingCtas)
     score_ring_kernel(const ScoreArgs p, const RingArgs q) {
@@ -747,13 +742,13 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
   constexpr int kB = ScoreType<DT>::kBytes, kPer = ScoreType<DT>::kPer16;
   constexpr int kT = NW * 32;
   constexpr int kIter = kStageIter;
-    extern __shared__ __align__(128) unsigned char ring[];
-  const RingLayout lay = ring_layout(q.stages);
+  extern __shared__ __align__(128) unsigned char ring[];
+  constexpr RingLayout lay = ring_layout();
   float4* part = reinterpret_cast<float4*>(ring + lay.part);  // [kSlots][C NW]
   RowGrad* grad = reinterpret_cast<RowGrad*>(ring + lay.grad);  // [kSlots], 32 bytes apart
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + lay.bars);
-  uint64_t* empty = full + q.stages;
-  uint64_t* sums_in = empty + q.stages;  // [kSlots] a row's sums have arrived
+  uint64_t* empty = full + kRingStages;
+  uint64_t* sums_in = empty + kRingStages;  // [kSlots] a row's sums have arrived
   uint64_t* result = sums_in + kSlots;   // [kSlots] its factors are there (no gradient: its sums are read)
   int* abort_flag = reinterpret_cast<int*>(ring + lay.flag);
 
@@ -762,7 +757,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
   const int rank = (int)cluster_rank();
   const int cid = blockIdx.x >> q.log2C, ncl = gridDim.x >> q.log2C;
   if (tid == 0) {
-    for (int s = 0; s < q.stages; ++s) {
+    for (int s = 0; s < kRingStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], NW);
     }
@@ -794,7 +789,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
   if (warp == NW) {
     // ------------------------------------------------------------ producer
     const uint64_t once = evict_first_policy(), again = evict_last_policy();
-    RingWalk walk{0, 1, q.stages, 0xffffffffu};  // an empty stage's first wait passes at once
+    RingWalk walk{0, 1, 0xffffffffu};  // an empty stage's first wait passes at once
     uint32_t fills = 0u;  // parity of each slot's copies
     // One stage of a share, granules g .. end - 1, into the walk's slot.
     auto copy_stage = [&](const RowShare& s, const char* img, int g, int end, uint64_t policy) {
@@ -856,10 +851,10 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
       const char* img = static_cast<const char*>(p.logits) + s.base;
       const int n_st = (s.n + kStageGran - 1) / kStageGran;
       const bool back = GRAD && !q.ahead;
-      const int kept = min(n_st, q.keep);
+      const int kept = min(n_st, kRingStages);
       for (int k = 0; k < n_st && ok; ++k)
         copy_stage(s, img, s.g0 + k * kStageGran, s.g0 + min(s.n, (k + 1) * kStageGran),
-                   (back && kept < n_st) || p.stats ? again : once);
+                   (back && k < n_st - kept) || p.stats ? again : once);
       if (back) {
         walk.turn();
         walk.step(kept);
@@ -870,7 +865,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
     if (!ok && lane == 0) fail();
     // every copy issued has landed before the CTA may leave
     if (lane == 0)
-      for (int k = 0; k < q.stages; ++k)
+      for (int k = 0; k < kRingStages; ++k)
         mbar_wait(&full[k], (fills >> k & 1u) ^ 1u, kDrainLimitNs);
     __syncwarp();
   } else if (warp == NW + 1) {
@@ -979,7 +974,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
     }
   } else {
     // ----------------------------------------------------------- consumers
-    RingWalk walk{0, 1, q.stages, 0u};
+    RingWalk walk{0, 1, 0u};
     int held = 0;        // ahead: the first slot still held
     uint32_t count = 0;  // rows folded
     // A folded row whose gradient is still to be written.
@@ -1019,7 +1014,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
       if (!q.ahead) walk.turn();
       for (int i = 0; i < n_st; ++i) {
         const int st_no = q.ahead ? i : n_st - 1 - i;  // the stage of the share
-        if (!q.ahead && i >= q.keep) {
+        if (!q.ahead && i >= kRingStages) {
           if (!wait(&full[walk.slot], walk.phase())) {
             ok = false;
             return;
@@ -1074,7 +1069,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[at]);
         if (q.ahead)
-          held = held + 1 == q.stages ? 0 : held + 1;
+          held = held + 1 == kRingStages ? 0 : held + 1;
         else
           walk.step();
       }
@@ -1127,7 +1122,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
       float za = 0.f;
       const int n_st = (sh.n + kStageGran - 1) / kStageGran;
       // stages that stay for the gradient: all (ahead), or the last ones
-      const int stay = !GRAD ? 0 : q.ahead ? n_st : min(n_st, q.keep);
+      const int stay = !GRAD ? 0 : q.ahead ? n_st : min(n_st, kRingStages);
       for (int k = 0; k < n_st; ++k) {
         if (!wait(&full[walk.slot], walk.phase())) {
           ok = false;
@@ -1192,7 +1187,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
       if (lane == 0) fail();
       // sums of this row may still be on their way to other CTAs: they land
       // well within this pause, before the barrier lets any CTA leave
-      __nanosleep(100000);
+      pause_ns(100000);
       __syncwarp();
     }
   }

@@ -739,6 +739,23 @@ def test_refusals(E, scorer):
     assert scorer.status() == 0
 
 
+@pytest.mark.parametrize("kw", [dict(temperature=1e-60), dict(temperature=1e60),
+                                dict(entropy_coef=1e60), dict(clip_high=1e60),
+                                dict(kl_coef=-1e60)])
+def test_values_past_fp32_are_refused(E, scorer, kw):
+    """Finite in 64 bits, but 0 or infinite as the fp32 the kernels use."""
+    z = torch.zeros((4, 64), device=DEV)
+    t = torch.zeros(4, dtype=torch.int32, device=DEV)
+    f = torch.zeros(4, device=DEV)
+    with pytest.raises(E.EBError):
+        scorer.policy_loss(z, t, f, f, ref_logprobs=f, **kw)
+    if "temperature" in kw:
+        h = torch.zeros((4, 8), dtype=BF16, device=DEV)
+        with pytest.raises(E.EBError):
+            scorer.lmhead_logprobs(h, torch.zeros((9, 8), dtype=BF16, device=DEV), t, **kw)
+    assert scorer.status() == 0
+
+
 def test_a_trajectory_is_sampled_scored_and_learned_from(E):
     """As the pieces are used together: a canvas is sampled, its committed
     tokens scored at their step's temperature (from logits and from hidden
