@@ -364,6 +364,10 @@ __device__ __forceinline__ void policy_total(const ScoreArgs& p, int leader,
 //              again, the most recent first, so that most come from L2 (the
 //              first copy asks L2 to keep them).
 //
+// Cluster c takes rows c, c + n, c + 2 n, ..., or (listed) the live rows number
+// c, c + n, ... and as even a part of the ignored ones, whose gradient is only
+// zeros to write: then every CTA counts the rows' liveness once, at the start.
+//
 // Rows start at any element.  A share is a range of 16-byte granules of the
 // row's 16-byte-aligned image; the granules that the row fills only partly
 // (at its two ends) are gathered element by element, with -inf in the places
@@ -377,6 +381,7 @@ constexpr int kStageGran = kRingWarps * 32 * kStageIter;
 constexpr int kStageBytes = kStageGran * 16;
 constexpr int kRingStages = 6;  // two CTAs of 96 KB rings share an SM
 constexpr int kMaxCluster = 16;
+constexpr int kListRows = 1024;  // of a cluster
 
 // A thread's reference is the maximum of what it folds first.  It moves only
 // when a fold's sum relative to it exceeds kMuch (or is not finite), so that
@@ -389,6 +394,7 @@ struct RingArgs {
   int mode;
   int log2C;     // CTAs per cluster: a power of two
   int ahead;     // two shares fit: the next row is folded before this one's gradient
+  int listed;    // the rows are shared out by lists, see below
 };
 
 // The ring's slots in their order of use, the same for the producer and the
@@ -412,7 +418,7 @@ struct RingWalk {
 constexpr int kSlots = 4;  // rows between a slot's uses, see the kernel
 
 struct RingLayout {
-  uint32_t part, grad, bars, flag, total;
+  uint32_t part, grad, bars, flag, count, list, total;
 };
 __host__ __device__ constexpr RingLayout ring_layout() {
   RingLayout y{};
@@ -420,7 +426,9 @@ __host__ __device__ constexpr RingLayout ring_layout() {
   y.grad = y.part + (uint32_t)(kSlots * kMaxCluster * kRingWarps * 16);
   y.bars = y.grad + kSlots * 32u;
   y.flag = y.bars + (2u * (uint32_t)kRingStages + 2u * kSlots) * 8u;
-  y.total = y.flag + 16u;
+  y.count = y.flag + 16u;
+  y.list = y.count + 16u * 4u;
+  y.total = y.list + (uint32_t)kListRows * 4u;
   return y;
 }
 
@@ -735,6 +743,46 @@ __device__ __forceinline__ RowShare row_share(const void* buf, int64_t ld, int r
   return s;
 }
 
+// The rows of cluster `cid`, where they are listed: its live ones, then its
+// ignored ones.  Returns how many, once every thread of the block has passed a
+// barrier; the list is complete after the next.
+__device__ __forceinline__ int list_rows(const ScoreArgs& p, const RingArgs& q,
+                                         const RowRange& range, int cid, int ncl, int* count,
+                                         int* list) {
+  if (!q.listed) return 0;
+  constexpr int kWarps = kRingThreads / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (p.rows + kWarps * 32 - 1) / (kWarps * 32) * 32;
+  const int r0 = min(p.rows, warp * per), r1 = min(p.rows, r0 + per);
+  auto lives = [&](int r) {
+    return __ballot_sync(0xffffffffu,
+                         r < r1 && range.live(r, p.tokens[r], p.weights ? p.weights[r] : 1.f));
+  };
+  int n = 0;
+#pragma unroll 8
+  for (int r = r0; r < r1; r += 32) n += __popc(lives(r + lane));
+  if (lane == 0) count[warp] = n;
+  __syncthreads();
+  int live = 0, before = 0;  // in all, and in the warps before this one
+  for (int w = 0; w < kWarps; ++w) {
+    if (w == warp) before = live;
+    live += count[w];
+  }
+  // the clusters with a live row fewer are the first to take an ignored one
+  const int back = ncl - 1 - cid;
+  const int mine = (live - cid + ncl - 1) / ncl;  // live rows
+#pragma unroll 4
+  for (int r = r0; r < r1; r += 32) {
+    const unsigned m = lives(r + lane);
+    const bool on = m >> lane & 1u;
+    const int ahead = before + __popc(m & ((1u << lane) - 1u));  // live rows before this one
+    const int rank = on ? ahead : r + lane - ahead, k = rank / ncl;
+    if (r + lane < r1 && rank - k * ncl == (on ? cid : back)) list[on ? k : mine + k] = r + lane;
+    before += __popc(m);
+  }
+  return mine + (p.rows - live - back + ncl - 1) / ncl;
+}
+
 template <int DT, bool ENT, bool GRAD>
 __global__ void __launch_bounds__(kRingThreads, kRingCtas)
     score_ring_kernel(const ScoreArgs p, const RingArgs q) {
@@ -751,6 +799,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
   uint64_t* sums_in = empty + kRingStages;  // [kSlots] a row's sums have arrived
   uint64_t* result = sums_in + kSlots;   // [kSlots] its factors are there (no gradient: its sums are read)
   int* abort_flag = reinterpret_cast<int*>(ring + lay.flag);
+  int* list = reinterpret_cast<int*>(ring + lay.list);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = 1 << q.log2C;
@@ -768,10 +817,15 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
     *abort_flag = 0;
     fence_mbar_init();
   }
+  const RowRange range = row_range(p);
+  const int n_rows = list_rows(p, q, range, cid, ncl, reinterpret_cast<int*>(ring + lay.count), list);
   __syncthreads();
   cluster_sync_all();
+  // this cluster's k-th row, or the number of rows
+  auto row_at = [&](int k) {
+    return !q.listed ? min(p.rows, cid + k * ncl) : k < n_rows ? list[k] : p.rows;
+  };
 
-  const RowRange range = row_range(p);
   auto fail = [&]() {
     atomicOr(p.status, kScoreTimeout);
     *(volatile int*)abort_flag = 1;
@@ -832,19 +886,20 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
       walk.used();
       walk.step();
     };
-    int i = cid;
+    int next = row_at(0);
     int token = -1;
     float weight = 1.f;
-    if (i < p.rows) {
-      token = p.tokens[i];
-      if (p.weights) weight = p.weights[i];
+    if (next < p.rows) {
+      token = p.tokens[next];
+      if (p.weights) weight = p.weights[next];
     }
-    for (; i < p.rows && ok; i += ncl) {
-      const int row = i;
+    for (int i = 1; next < p.rows && ok; ++i) {
+      const int row = next;
       const bool on = range.live(row, token, weight);
-      if (i + ncl < p.rows) {
-        token = p.tokens[i + ncl];
-        if (p.weights) weight = p.weights[i + ncl];
+      next = row_at(i);
+      if (next < p.rows) {
+        token = p.tokens[next];
+        if (p.weights) weight = p.weights[next];
       }
       if (!on) continue;
       const RowShare s = row_share<DT>(p.logits, p.ld, row, p.V, q.log2C, rank);
@@ -889,14 +944,15 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
           if (p.g_h) x1 = p.g_h[row];
         }
       };
-      int i = cid;
-      if (i < p.rows) fetch(i);
-      for (; i < p.rows && ok; i += ncl) {
-        const int row = i;
+      int next = row_at(0);
+      if (next < p.rows) fetch(next);
+      for (int i = 1; next < p.rows && ok; ++i) {
+        const int row = next;
         const int a = token;
         const float wt = weight, y0 = x0, y1 = x1, y2 = x2;
         const float Trow = row_temp_ok(T) ? T : nan;
-        if (i + ncl < p.rows) fetch(i + ncl);
+        next = row_at(i);
+        if (next < p.rows) fetch(next);
         if (!range.live(row, a, wt)) {
           if (first && lane == 0) {
             if (p.logprobs) p.logprobs[row] = 0.f;
@@ -1075,23 +1131,24 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
       }
     };
 
-    int i = cid;
+    int next = row_at(0);
     int token = -1;
     float weight = 1.f, T = p.temp;
-    if (i < p.rows) {
-      token = p.tokens[i];
-      if (p.weights) weight = p.weights[i];
-      if (p.temps) T = p.temps[i];
+    if (next < p.rows) {
+      token = p.tokens[next];
+      if (p.weights) weight = p.weights[next];
+      if (p.temps) T = p.temps[next];
     }
-    for (; i < p.rows && ok; i += ncl) {
-      const int row = i;
+    for (int i = 1; next < p.rows && ok; ++i) {
+      const int row = next;
       const int a = token;
       const float wt = weight;
       const float c2 = log2e_over(row_temp_ok(T) ? T : nan);
-      if (i + ncl < p.rows) {
-        token = p.tokens[i + ncl];
-        if (p.weights) weight = p.weights[i + ncl];
-        if (p.temps) T = p.temps[i + ncl];
+      next = row_at(i);
+      if (next < p.rows) {
+        token = p.tokens[next];
+        if (p.weights) weight = p.weights[next];
+        if (p.temps) T = p.temps[next];
       }
       const RowShare sh = row_share<DT>(p.logits, p.ld, row, p.V, q.log2C, rank);
       if (!range.live(row, a, wt)) {

@@ -263,6 +263,43 @@ def test_many_rows_in_turn(scorer, dtype, rows, V):
     assert scorer.status() == 0
 
 
+@pytest.mark.parametrize("ignored", ["scattered", "head", "all but one", "all", "none"])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_long_calls_share_out_their_live_rows(scorer, dtype, ignored):
+    """Enough rows that they are shared out by lists of live and ignored ones:
+    each row's results are its own, wherever the ignored ones lie."""
+    rows, V = 1003, 131072 if dtype is BF16 else 65601
+    z, tokens, _ = R.make_logits(rows, V, dtype, 17, DEV)
+    keep = torch.ones(rows, dtype=torch.bool)
+    if ignored == "scattered":
+        keep = torch.rand(rows, generator=torch.Generator().manual_seed(4)) < 0.7
+    elif ignored == "head":
+        keep[:611] = False
+    elif ignored != "none":
+        keep[:] = False
+        keep[777] = ignored == "all but one"
+    tokens = torch.where(keep.to(DEV), tokens, -1)
+    g = randn(rows, 1)
+    weights = torch.where(keep.to(DEV), 1.0, 0.0)
+    _, _, old, _, adv = policy_inputs(scorer, rows, 8, F32, 5)
+    r = scorer.token_logprobs(z, tokens, temperature=0.8)
+    d = scorer.token_logprobs_backward(z, tokens, g, temperature=0.8)
+    p = scorer.policy_loss(z, tokens.clamp(min=0), old, adv, weights=weights, temperature=0.8,
+                           entropy_coef=0.01, scale=0.01)
+    for lo in range(0, rows, 128):
+        at = slice(lo, lo + 128)
+        check_scores(type(r)(r.logprobs[at], r.entropies[at]), z[at], 0.8, tokens[at])
+        check_scores(type(r)(p.logprobs[at], p.entropies[at]), z[at], 0.8, tokens[at])
+        R.check_gradient(d[at], *R.gradient(z[at], 0.8, tokens[at], g[at], None), dtype)
+    gone = (~keep).to(DEV)
+    assert (p.d_logits[gone] == 0).all()
+    # the same bits again
+    q = scorer.policy_loss(z, tokens.clamp(min=0), old, adv, weights=weights, temperature=0.8,
+                           entropy_coef=0.01, scale=0.01)
+    assert torch.equal(p.terms, q.terms) and torch.equal(p.d_logits, q.d_logits)
+    assert scorer.status() == 0
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_in_place_gradient_equals_the_separate_one(scorer, dtype):
     for rows, V in ((5, 1000), (40, 32003), (3, 262144)):
