@@ -955,9 +955,9 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
           if (p.g_h) x1 = p.g_h[row];
         }
       };
-      int next = row_at(0);
+      int next = row_at(0), i = 1;
       if (next < p.rows) fetch(next);
-      for (int i = 1; next < p.rows && ok; ++i) {
+      for (; next < p.rows && ok; ++i) {
         const int row = next;
         const int a = token;
         const float wt = weight, y0 = x0, y1 = x1, y2 = x2;
@@ -1037,7 +1037,16 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
         }
         ++count;
       }
-      if (!ok && lane == 0) fail();
+      if (!ok) {
+        // the rows left, this one first: NaN, not what was there before
+        if (lane == 0) fail();
+        for (int k = i - 1 + lane; first && row_at(k) < p.rows; k += 32) {
+          const int row = row_at(k);
+          if (p.logprobs) p.logprobs[row] = nan;
+          if (p.entropies) p.entropies[row] = nan;
+          if (p.stats) p.stats[row] = make_float4(nan, nan, nan, nan);
+        }
+      }
     }
   } else {
     // ----------------------------------------------------------- consumers
@@ -1048,7 +1057,8 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
     struct Pending {
       int row, token;
       float c2;
-    } last{-1, 0, 0.f};
+      int k;  // its number among this cluster's rows
+    } last{-1, 0, 0.f, 0};
 
     // The token's place in this CTA's share: this thread's granule (counted
     // along its own granules, -1: another thread's) and element.
@@ -1142,7 +1152,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
       }
     };
 
-    int next = row_at(0);
+    int next = row_at(0), i = 1;
     int token = -1;
     float weight = 1.f, T = p.temp;
     if (next < p.rows) {
@@ -1150,7 +1160,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
       if (p.weights) weight = p.weights[next];
       if (p.temps) T = p.temps[next];
     }
-    for (int i = 1; next < p.rows && ok; ++i) {
+    for (; next < p.rows && ok; ++i) {
       const int row = next;
       const int a = token;
       const float wt = weight;
@@ -1240,7 +1250,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
                   map_rank(smem_u32(&sums_in[par]), lane));
       }
       if (GRAD) {
-        const Pending now{row, a, c2};
+        const Pending now{row, a, c2, i - 1};
         if (!q.ahead)
           write_grad(now, count);
         else if (last.row >= 0)
@@ -1256,6 +1266,16 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
       // sums of this row may still be on their way to other CTAs: they land
       // well within this pause, before the barrier lets any CTA leave
       pause_ns(100000);
+      // this warp's first granule of each row whose gradient it has not finished: NaN
+      for (int k = q.ahead && last.row >= 0 ? last.k : i - 1;
+           GRAD && lane == 0 && row_at(k) < p.rows; ++k) {
+        const RowShare sh = row_share<DT>(p.logits, p.ld, row_at(k), p.V, q.log2C, rank);
+        for (int e = 0; tid < sh.n && e < kPer; ++e) {
+          const int v = (sh.g0 + tid) * kPer + e - sh.shift;
+          if (v >= 0 && v < p.V)
+            store_grad<DT>(grad_image(row_at(k), sh), (int64_t)(sh.g0 + tid) * kPer + e, nan);
+        }
+      }
       __syncwarp();
     }
   }

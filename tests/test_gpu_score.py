@@ -726,6 +726,48 @@ def test_a_wait_that_runs_out_is_reported(E):
     sc.close()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,V", [(300, 20001), (40, 262144), (1003, 131072)])
+def test_a_pass_cut_short_leaves_nan(E, dtype, rows, V):
+    """Rows that a pass did not reach hold NaN, not what was in the buffers
+    before: each row's results are the right ones or NaN, and without NaN no
+    wait was reported.  (A wait tests its barrier once whatever its limit, and
+    that test may last until the copy has come: whether a given wait gives up
+    is not promised.)"""
+    sc = E.EBScorer(rows, device=DEV)
+    z, tokens, _ = R.make_logits(rows, V, dtype, 9, DEV)
+    g = randn(rows, 1)
+    off = torch.tensor([0, rows // 2, rows], dtype=torch.int32, device=DEV)
+    want = sc.token_logprobs(z, tokens)
+    d = sc.token_logprobs_backward(z, tokens, g)
+    assert sc.status() == 0
+
+    def right_or_nan(got, ref):
+        nan = torch.isnan(got).view(rows, -1).any(1)
+        assert torch.equal(nan, ~(got == ref).view(rows, -1).all(1))
+        assert sc.status(clear=True) & E.STATUS_TIMEOUT or not nan.any()
+
+    sc.set_wait_limit(1)
+    stale = [torch.full((rows,), 7.0, device=DEV) for _ in range(4)]
+    del stale  # the results' memory, as the allocator hands it out next
+    lp, H = sc.token_logprobs(z, tokens)
+    assert torch.equal(torch.isnan(lp), torch.isnan(H))
+    assert torch.equal(H[~torch.isnan(H)], want.entropies[~torch.isnan(H)])
+    right_or_nan(lp, want.logprobs)
+    out = torch.full_like(d, 7.0)
+    right_or_nan(sc.token_logprobs_backward(z, tokens, g, out=out), d)
+    r = sc.preference_loss(z, tokens, off, out=out.fill_(7.0))
+    sc.status(clear=True)
+    left = torch.isnan(r.logprobs).any()
+    assert torch.isnan(r.loss).all() == left and torch.isnan(r.losses).all() == left
+    assert torch.isnan(r.d_logits).any(1).all() == left  # the pair's factor is NaN
+    assert (r.d_logits != 7.0).all(1).all()
+    sc.set_wait_limit(0)
+    again = sc.token_logprobs(z, tokens)
+    assert torch.equal(again.logprobs, want.logprobs) and sc.status() == 0
+    sc.close()
+
+
 def test_refusals(E, scorer):
     z = torch.zeros((4, 64), device=DEV)
     t = torch.zeros(4, dtype=torch.int32, device=DEV)
