@@ -517,6 +517,32 @@ def test_bad_offsets_are_reported_and_stay_inside(scorer):
     assert scorer.status() == 0
 
 
+@pytest.mark.parametrize("rows,pairs", [(512, 64), (513, 3), (130, 65), (512, 1)])
+def test_few_and_many_pairs(scorer, rows, pairs):
+    """One pair to many: the losses, their factors, and a pair out of order among
+    good ones."""
+    z, tokens, _ = R.make_logits(rows, 700, F32, 5, DEV)
+    cuts = torch.linspace(0, rows, 2 * pairs + 1).int()
+    lp, _ = R.scores(z, 0.7, tokens)
+    off = cuts.to(DEV)
+    r = scorer.preference_loss(z, tokens, off, temperature=0.7, **PREF)
+    loss, losses, S, g = R.preference(lp, tokens, off, None, 0.2, 0.1, 0.05, False, 1.0)
+    tl, _ = R.logprob_tol(z, 0.7, tokens)
+    tm = 0.2 * 2 * float(tl.sum()) + 1e-12
+    assert ((r.losses.double() - losses).abs() <= tm + R.U * losses.abs()).all()
+    assert abs(float(r.loss) - float(loss)) <= pairs * tm + 4 * R.U * abs(float(loss))
+    d, tol = R.gradient(z, 0.7, tokens, g, None)
+    R.check_gradient(r.d_logits, d, tol + d.abs() * (tm + 2 * R.U) + 0.2 * 0.1 * tm * (d != 0), F32)
+    wrong = cuts.clone()
+    wrong[1] = rows + 1  # the first sequence's end: out of range, the second's start too
+    r2 = scorer.preference_loss(z, tokens, wrong.to(DEV), temperature=0.7, **PREF)
+    assert scorer.status(clear=True) & 8
+    assert torch.isnan(r2.loss).all() and torch.isnan(r2.losses[0])
+    assert torch.equal(r2.losses[2:], r.losses[2:])
+    assert torch.equal(scorer.preference_loss(z, tokens, off, temperature=0.7, **PREF).loss, r.loss)
+    assert scorer.status() == 0
+
+
 @pytest.mark.parametrize("rows,V,d", [(1, 1, 8), (1, 256, 64), (3, 255, 72), (24, 1000, 128),
                                       (128, 513, 200), (129, 4096, 64), (300, 5000, 264),
                                       (257, 2047, 2560), (600, 32003, 128), (2, 70001, 64),
@@ -730,8 +756,8 @@ def test_a_wait_that_runs_out_is_reported(E):
 @pytest.mark.parametrize("rows,V", [(300, 20001), (40, 262144), (1003, 131072)])
 def test_a_pass_cut_short_leaves_nan(E, dtype, rows, V):
     """Rows that a pass did not reach hold NaN, not what was in the buffers
-    before: each row's results are the right ones or NaN, and without NaN no
-    wait was reported.  (A wait tests its barrier once whatever its limit, and
+    before: each row's results are the right ones, or NaN where a wait was
+    reported.  (A wait tests its barrier once whatever its limit, and
     that test may last until the copy has come: whether a given wait gives up
     is not promised.)"""
     sc = E.EBScorer(rows, device=DEV)
