@@ -53,7 +53,7 @@ const void* const kShort[2][kVariants] = {
 
 using ebk::kListRows;
 using ebk::kRingStages;
-constexpr double kListUs = 60.0;
+constexpr double kListUs = 100.0;
 constexpr int kMaxLog2C = 4;
 
 struct DeviceInfo {
@@ -294,8 +294,8 @@ int launch_rows(const eb_scorer* h, const ScoreArgs& a, int dtype, int mode, boo
   q.ahead = 2 * share_stages(row_bytes, c) <= kRingStages;
   // Rows shared out by lists: where a cluster takes more than two, and the launch
   // is long enough for the counting (2048 rows of 262144 bf16 with gradient:
-  // none ignored 416 us against 411, 128 scattered ones 397 against 416, 512
-  // 354 against 395).
+  // none ignored 416 us against 410, 128 scattered ones 396 against 413, 512
+  // 352 against 390; 1000 rows, scores, none ignored: 96.6 against 93.8).
   const int clusters = std::max(1, std::min(a.rows, most));
   q.listed = a.rows > 2 * clusters && us > kListUs && a.rows <= (kListRows - 2) * clusters;
   cudaLaunchConfig_t lc;

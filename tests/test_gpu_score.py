@@ -268,7 +268,7 @@ def test_many_rows_in_turn(scorer, dtype, rows, V):
 def test_long_calls_share_out_their_live_rows(scorer, dtype, ignored):
     """Enough rows that they are shared out by lists of live and ignored ones:
     each row's results are its own, wherever the ignored ones lie."""
-    rows, V = 1003, 131072 if dtype is BF16 else 65601
+    rows, V = 2050, 131072 if dtype is BF16 else 65601
     z, tokens, _ = R.make_logits(rows, V, dtype, 17, DEV)
     keep = torch.ones(rows, dtype=torch.bool)
     if ignored == "scattered":
