@@ -17,8 +17,9 @@
 // truncation: about 2^-26 of the sum lost per step, always toward zero (1.6e-8
 // measured; over the 160 steps of d = 2560 a logit of 10 was 2.6e-5 low, five
 // times what fp32 summation loses).  So an accumulator takes 512 elements of
-// K at most, and the pieces are added in registers, rounded to nearest (1 % of
-// the time of 2048 rows against 1024 elements, for half the error).
+// K at most, and the pieces are added in registers, rounded to nearest (2048
+// rows: 3 % of the time against 1024 elements, for half the error; 256 elements
+// would take 15 % more).
 //
 // Where a pair's product would be half padding (65 to 128 rows, and small odd
 // numbers of 128-row tiles) each CTA works alone, with M = 128.
@@ -32,13 +33,11 @@
 // lmscore_finish_kernel.
 //
 // What bounds them, at 262144 ids and d = 2560: up to 64 rows the reading of W
-// (24 rows 219 us, 6.1 TB/s, 0.93 of the measured copy rate).  Above that the
-// tensor cores, and under a steady load the chip's power: 256 rows 338 us (288
-// in a short burst, at 1.2 PFLOP/s), 2048 rows 2.26 ms (1.22 PFLOP/s, 0.87 of
-// what a library product sustains).  A stage costs a CTA 32 KB from L2 for 512
-// cycles of MMA, about what an SM can take; holding more of W per stage would
-// need the TMEM that the second accumulator has, and without it the epilogue
-// does not overlap.
+// (24 rows 213 us, 6.3 TB/s, 0.96 of the measured copy rate).  Above that the
+// tensor cores (85 % busy at 512 rows), and under a steady load the chip's
+// power: 256 rows 338 us (277 in a short burst, at 1.24 PFLOP/s), 2048 rows
+// 2.05 ms (1.34 PFLOP/s, 0.96 of what a library product sustains).  W asked for
+// in L2 some stages ahead: 5 to 15 % slower.
 #pragma once
 
 #include "eb_score.cuh"
@@ -464,8 +463,8 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kLsThread
 // warps meet once, at the end.
 // ---------------------------------------------------------------------------
 constexpr int kLfRows = 64;
-// Stages of one accumulator: 256 elements of K, for half the truncation of 512 and
-// 2 % of the time (24 rows of 262144 x 2560: 236 us against 231; 128 elements: 244).
+// Stages of one accumulator: 256 elements of K, for half the truncation of 512
+// (24 rows of 262144 x 2560: 212 us; 128 elements 219).
 constexpr int kLfChunk = 4;
 constexpr int kLfPer = 16;  // rows per epilogue thread
 // Within +-kDeep; NaN stays NaN.

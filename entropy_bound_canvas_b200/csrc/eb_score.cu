@@ -538,10 +538,11 @@ int eb_lmhead_logprobs(eb_scorer_t* h, const void* hidden, const void* weight, i
   p.logprobs = logprobs;
   p.entropies = entropies;
   // An odd number of 128-row tiles leaves half of the last pair's work padding;
-  // single CTAs take 8 % longer for the same tiles (2048 rows: 2.46 ms against
-  // 2.27), so they win up to 11 tiles (300 rows: 0.51 ms against 0.58).
+  // single CTAs take longer for the same tiles, so they win up to 9 tiles (262144
+  // ids, d = 2560: 300 rows 489 us against 539 on pairs, 1100 rows 1303 against
+  // 1331, 1400 rows 1695 against 1570).
   const int tiles = (rows + ebk::kLsRows - 1) / ebk::kLsRows;
-  const bool few = rows <= ebk::kLfRows, pair = tiles % 2 == 0 || tiles > 11;
+  const bool few = rows <= ebk::kLfRows, pair = tiles % 2 == 0 || tiles > 9;
   if (few) {
     p.n_split = std::min(h->sms, (V + 127) / 128);
     p.n_rec = p.n_split;
