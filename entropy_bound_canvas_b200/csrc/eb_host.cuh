@@ -35,6 +35,22 @@ struct DeviceGuard {
 
 inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Zeros device memory of the current device before it returns, whatever the
+// device's other streams hold.  (cudaMemset on device memory returns early, on
+// a stream that non-blocking streams do not wait for: a handle's first call
+// could be under way when its workspace is cleared.)
+inline bool clear_now(void* p, size_t bytes) {
+  cudaStream_t st = nullptr;
+  bool ok = cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking) == cudaSuccess;
+  if (ok) {
+    ok = cudaMemsetAsync(p, 0, bytes, st) == cudaSuccess;
+    ok = cudaStreamSynchronize(st) == cudaSuccess && ok;
+    ok = cudaStreamDestroy(st) == cudaSuccess && ok;
+  }
+  if (!ok) cudaGetLastError();
+  return ok;
+}
+
 // A kernel launched as a programmatic dependent of the previous one on `st`.
 inline bool launch_dependent(const void* fn, dim3 grid, dim3 block, size_t smem, void** args,
                              cudaStream_t st) {

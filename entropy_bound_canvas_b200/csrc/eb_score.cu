@@ -351,7 +351,7 @@ int eb_scorer_init(eb_scorer_t** out, int32_t max_rows, int device) {
     delete h;
     return EB_ERR_OUT_OF_MEMORY;
   }
-  if (cudaMemset(h->ws, 0, h->ws_bytes) != cudaSuccess) {
+  if (!ebk::clear_now(h->ws, h->ws_bytes)) {
     cudaFree(h->ws);
     delete h;
     return EB_ERR_CUDA;

@@ -387,7 +387,8 @@ typedef struct {
 } eb_score_input_t;
 
 /* Create a scorer on CUDA device `device` (sm_100) for calls of up to
-   max_rows rows (1 .. EB_MAX_SCORE_ROWS); one device allocation.
+   max_rows rows (1 .. EB_MAX_SCORE_ROWS); one device allocation, cleared
+   before this returns (so not while a stream is being captured).
    Errors: INVALID_ARG, OVERFLOW, UNSUPPORTED, OUT_OF_MEMORY, CUDA. */
 int eb_scorer_init(eb_scorer_t** out, int32_t max_rows, int device);
 
