@@ -283,7 +283,7 @@ int eb_sampler_init(eb_sampler_t** out, const eb_config_t* cfg, int device) {
     delete h;
     return EB_ERR_OUT_OF_MEMORY;
   }
-  if (cudaMemset(h->ws, 0, h->ws_bytes) != cudaSuccess) {
+  if (!ebk::clear_now(h->ws, h->ws_bytes)) {
     cudaFree(h->ws);
     delete h;
     return EB_ERR_CUDA;

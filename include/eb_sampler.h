@@ -140,7 +140,8 @@ void eb_config_default(eb_config_t* cfg, int32_t B, int32_t L, int32_t V);
    Validates cfg, allocates and zeroes the workspace (the per-(position,
    stream CTA) records and per-position counters of the stream pass, the
    active-canvas list, previous argmax, stability counters, per-position
-   draws and max probabilities, status word) in one allocation.  The first
+   draws and max probabilities, status word) in one allocation, cleared before
+   this returns (so not while a stream is being captured).  The first
    handle on a device also sets the kernels' shared-memory attributes for
    that device (once, to the device maximum).
    On success *out owns the handle (release with eb_sampler_destroy).

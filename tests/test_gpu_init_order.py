@@ -69,3 +69,28 @@ def test_a_scorer_made_while_the_default_stream_is_busy(E):
     assert status == 0
     for got in (first, again):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_sampler_made_while_the_default_stream_is_busy(E):
+    B, L, V, steps = 2, 16, 8200, 6
+    g = torch.Generator().manual_seed(4)
+    logits = (2.0 * torch.randn((steps, B, L, V), generator=g)).to(torch.bfloat16).to(DEV)
+    logits[:, :, ::2, 5] += 14.0
+
+    def use(eb):
+        canvas, committed, stop = eb.new_canvas()
+        H, amax = (t.zero_() for t in eb.outputs())
+        out = []
+        for s in range(steps):
+            eb.step(logits[s], s, canvas, committed, H, amax, stop)
+            out += [t.clone() for t in (canvas, committed, H, amax, stop)]
+        return out
+
+    def make():
+        return E.EBSampler(B, L, V, device=DEV, num_steps=steps, seed=3)
+
+    want, _, _ = made_and_used(False, make, use)
+    first, again, status = made_and_used(True, make, use)
+    assert status == 0
+    for got in (first, again):
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
