@@ -212,6 +212,13 @@ def _torch():
     return torch
 
 
+def _cuda_device(device):
+    """The CUDA device of this index: the current one where none is named."""
+    torch = _torch()
+    index = None if device is None else torch.device(device).index
+    return torch.device("cuda", torch.cuda.current_device() if index is None else index)
+
+
 def lmhead_logits(hidden, weight, out=None):
     """The LM head's logits hidden @ weight^T (bf16 [rows, d] and [V, d] on
     one device) formed by the fused LM-head kernel's tensor-core contraction,
@@ -246,8 +253,7 @@ class EBSampler:
 
     def __init__(self, B: int, L: int, V: int, device=None, **config):
         torch = _torch()
-        self.device = torch.device("cuda", torch.cuda.current_device() if device is None
-                                   else torch.device(device).index or 0)
+        self.device = _cuda_device(device)
         self.cfg = make_config(B, L, V, **config)
         self.B, self.L, self.V = B, L, V
         h = C.c_void_p()
@@ -509,8 +515,7 @@ class EBScorer:
 
     def __init__(self, max_rows: int, device=None):
         torch = _torch()
-        self.device = torch.device("cuda", torch.cuda.current_device() if device is None
-                                   else torch.device(device).index or 0)
+        self.device = _cuda_device(device)
         self.max_rows = int(max_rows)
         h = C.c_void_p()
         _check(_lib().eb_scorer_init(C.byref(h), self.max_rows, self.device.index),
