@@ -842,9 +842,19 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
     *(volatile int*)abort_flag = 1;
   };
   // A barrier's phase has completed: one test and a vote, the bounded wait
-  // only where that fails.  The outcome is the whole warp's.
+  // only where that fails.  The outcome is the whole warp's.  The test may
+  // suspend the thread until the phase completes, whatever the limit.
   auto wait = [&](uint64_t* bar, uint32_t ph) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, ph))) return true;
+    return (bool)__all_sync(0xffffffffu, mbar_wait_timed(bar, ph, p.wait_ns, abort_flag));
+  };
+  // The same, but a limit shorter than that is kept: the finisher's wait for a
+  // row's sums, which are never there at its first test, so that a short limit
+  // runs out in every call.  In every wait the look at the limit costs up to
+  // 3 % (2048 rows of 262144 bf16, scores: 194.6 us against 188.4), in this one
+  // nothing (188.4).
+  auto wait_limited = [&](uint64_t* bar, uint32_t ph) {
+    if (p.wait_ns >= kSuspendHintNs) return wait(bar, ph);
     return (bool)__all_sync(0xffffffffu, mbar_wait_timed(bar, ph, p.wait_ns, abort_flag));
   };
   bool ok = true;
@@ -976,7 +986,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
         const float c2 = sc.c2;
         if (lane == 0) mbar_arrive_expect_tx(&sums_in[par], (uint32_t)(C * NW * 16));
         __syncwarp();
-        if (!wait(&sums_in[par], ph)) {
+        if (!wait_limited(&sums_in[par], ph)) {
           ok = false;
           break;
         }

@@ -1,0 +1,68 @@
+"""The row kernels keep a short wait limit: each call on rows that are copied
+into shared memory reports the wait that ran out, and leaves the right result
+or NaN."""
+from __future__ import annotations
+
+import pytest
+
+import score_ref as R
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def E():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    from entropy_bound_canvas_b200 import build as B
+    B.build()
+    import entropy_bound_canvas_b200 as E
+    return E
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,V", [(1, 20001), (300, 20000), (40, 262144), (1003, 131072)])
+def test_every_call_reports_a_short_limit(E, dtype, rows, V):
+    """One CTA's row and rows on clusters, one round of them and several, shares
+    inside the ring and past it."""
+    sc = E.EBScorer(rows + 1, device=DEV)
+    z, tokens, _ = R.make_logits(rows, V, dtype, 9, DEV)
+    lp, _ = sc.token_logprobs(z, tokens)
+    adv = torch.ones(rows, device=DEV)
+    off = torch.tensor([0, rows // 2, rows], dtype=torch.int32, device=DEV)
+    out = torch.empty_like(z, memory_format=torch.contiguous_format)
+
+    def calls():
+        yield "scores", lambda: sc.token_logprobs(z, tokens)
+        yield "alone", lambda: sc.token_logprobs(z, tokens, entropies=False)
+        yield "back", lambda: [sc.token_logprobs_backward(z, tokens, adv, adv, out=out)]
+        yield "back alone", lambda: [sc.token_logprobs_backward(z, tokens, adv, out=out)]
+        yield "policy", lambda: sc.policy_loss(z, tokens, lp, adv, entropy_coef=0.1, out=out)
+        yield "loss", lambda: sc.policy_loss(z, tokens, lp, adv, grad=False)
+        yield "preference", lambda: sc.preference_loss(z, tokens, off, out=out)
+
+    for name, call in calls():
+        want = [None if t is None else t.clone() for t in call()]
+        assert sc.status() == 0, name
+        for limit in (1, 100):
+            out.fill_(7.0)
+            sc.set_wait_limit(limit)
+            got = call()
+            assert sc.status(clear=True) & E.STATUS_TIMEOUT, (name, limit)
+            assert any(torch.isnan(t).any() for t in got if t is not None), (name, limit)
+            if name in ("policy", "loss"):
+                assert torch.isnan(got[0]).all()
+            if name != "preference":  # there one NaN row is its pair's, so every row's
+                for a, b in zip(got, want):
+                    if a is not None:
+                        assert ((a == b) | torch.isnan(a)).view(a.shape[0], -1).all(1)[
+                            ~torch.isnan(a).view(a.shape[0], -1).any(1)].all(), name
+            sc.set_wait_limit(0)
+            again = call()
+            assert sc.status() == 0, (name, limit)
+            assert all(a is None or torch.equal(a, b) for a, b in zip(again, want)), name
+    sc.close()
