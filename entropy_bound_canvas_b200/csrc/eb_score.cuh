@@ -251,48 +251,115 @@ __device__ __forceinline__ RowRange row_range(const ScoreArgs& p) {
 // The policy loss of a row.
 //   L = w [ max(-A r, -A clip(r)) + k KL - c H ],  r = exp(log p_a - old),
 //   KL = exp(ref - log p_a) - 1 - (ref - log p_a)
+// Formed in fp32 near the policy that drew the token.  Where the exponents or
+// their products leave fp32's range (kFarExp, kFarSize), the row is `far`, and
+// policy_far forms it in 64 bits: w may bring an A r past fp32 back into it.
+// A factor of 0 takes its term out, whatever the term: an advantage of 0 beside
+// an infinite ratio, a k of 0 beside an infinite KL.
+constexpr float kFarExp = 80.0f, kFarSize = 1e30f;
+
 struct PolicyRow {
   float pg, kl, dkl;
   bool cut;  // the clipped side is the larger: no gradient through the ratio
+  bool far;  // fp32 does not hold it: policy_far does
+};
+struct PolicyFar {
+  double pg, kl, dkl;
+  bool cut;
 };
 
 __device__ __forceinline__ PolicyRow policy_row(const ScoreArgs& p, const RowResult& r,
-                                                float old_lp, float adv, float ref_lp) {
-  const float ratio = expf((r.lp - old_lp) + r.lp_low);
+                                                float old_lp, float adv, float ref_lp,
+                                                float weight) {
+  const float x = (r.lp - old_lp) + r.lp_low;
+  const float ratio = expf(x);
   const float free = -adv * ratio;
-  // the comparisons keep a NaN ratio NaN
   const float held_ratio = ratio < p.clip_lo ? p.clip_lo : ratio > p.clip_hi ? p.clip_hi : ratio;
   const float held = -adv * held_ratio;
   PolicyRow o;
   o.cut = held > free;
   o.pg = o.cut ? held : free;
   o.kl = o.dkl = 0.f;
+  float reach = fabsf(x);
   if (p.ref_lp) {
     const float gap = (ref_lp - r.lp) - r.lp_low;
     const float back = expm1f(gap);
     o.kl = back - gap;
     o.dkl = -back;
+    reach += fabsf(gap);
+  }
+  // NaN is far, and so is a w that scale or weight brings past fp32's middle
+  const float w = fabsf(weight * (float)p.scale);
+  const bool near = reach < kFarExp && fabsf(o.pg) < kFarSize &&
+                    w < kFarSize && w > 1.f / kFarSize;
+  o.far = !near;
+  return o;
+}
+
+static __device__ __noinline__ PolicyFar policy_far(float lp, float lp_low, float old_lp,
+                                                    float adv, float ref_lp, bool has_ref,
+                                                    float clip_lo, float clip_hi) {
+  PolicyFar o;
+  const double x = ((double)lp - (double)old_lp) + (double)lp_low;
+  const double ratio = exp(x), A = (double)adv;
+  // the comparisons keep a NaN ratio NaN
+  const double held_ratio =
+      ratio < (double)clip_lo ? (double)clip_lo : ratio > (double)clip_hi ? (double)clip_hi : ratio;
+  double free = -A * ratio, held = -A * held_ratio;
+  if (A == 0.0 && x == x) free = held = 0.0;
+  o.cut = held > free;
+  o.pg = o.cut ? held : free;
+  o.kl = o.dkl = 0.0;
+  if (has_ref) {
+    const double gap = ((double)ref_lp - (double)lp) - (double)lp_low;
+    const double back = expm1(gap);
+    o.kl = back < (double)INFINITY ? back - gap : back;
+    o.dkl = -back;
   }
   return o;
 }
 
-__device__ __forceinline__ RowCoef policy_coef(const ScoreArgs& p, const PolicyRow& o,
-                                               float weight) {
-  const float w = weight * (float)p.scale;
+// The factors of log p_a and H in the gradient.
+__device__ __forceinline__ RowCoef policy_coef(const ScoreArgs& p, const RowResult& r,
+                                               const PolicyRow& o, float old_lp, float adv,
+                                               float ref_lp, float weight) {
   RowCoef c;
-  c.g = w * fmaf(p.kl_coef, o.dkl, o.cut ? 0.f : o.pg);
-  c.h = -w * p.ent_coef;
+  if (!o.far) {
+    const float w = weight * (float)p.scale;
+    c.g = w * fmaf(p.kl_coef, o.dkl, o.cut ? 0.f : o.pg);
+    c.h = -w * p.ent_coef;
+  } else {
+    const PolicyFar f = policy_far(r.lp, r.lp_low, old_lp, adv, ref_lp, p.ref_lp != nullptr,
+                                   p.clip_lo, p.clip_hi);
+    const double w = (double)weight * p.scale;
+    double g = f.cut ? 0.0 : f.pg;
+    if (p.kl_coef != 0.f) g += (double)p.kl_coef * f.dkl;
+    c.g = (float)(w * g);
+    c.h = (float)(-w * (double)p.ent_coef);
+  }
   return c;
 }
 
-__device__ __forceinline__ void policy_add(const ScoreArgs& p, const PolicyRow& o, float H,
-                                           float weight, double (&t)[kPolicyTerms]) {
+__device__ __forceinline__ void policy_add(const ScoreArgs& p, const RowResult& r,
+                                           const PolicyRow& o, float old_lp, float adv,
+                                           float ref_lp, float weight,
+                                           double (&t)[kPolicyTerms]) {
   const double w = (double)weight * p.scale;
-  t[0] += w * ((double)o.pg + (double)p.kl_coef * o.kl - (double)p.ent_coef * H);
-  t[1] += w * o.pg;
-  t[2] += w * o.kl;
-  t[3] += w * H;
-  t[4] += o.cut ? w : 0.0;
+  double pg = o.pg, kl = o.kl;
+  bool cut = o.cut;
+  if (o.far) {
+    const PolicyFar f = policy_far(r.lp, r.lp_low, old_lp, adv, ref_lp, p.ref_lp != nullptr,
+                                   p.clip_lo, p.clip_hi);
+    pg = f.pg;
+    kl = f.kl;
+    cut = f.cut;
+  }
+  const double k = p.kl_coef == 0.f ? 0.0 : (double)p.kl_coef * kl;
+  t[0] += w * (pg + k - (double)p.ent_coef * r.H);
+  t[1] += w * pg;
+  t[2] += w * kl;
+  t[3] += w * r.H;
+  t[4] += cut ? w : 0.0;
 }
 
 // The loss's terms.  A CTA's part is the sum of its leaders' t (one thread
@@ -813,6 +880,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
   int* list = reinterpret_cast<int*>(ring + lay.list);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool is_policy = ENT && q.mode == kModePolicy;  // always with entropies
   const int C = 1 << q.log2C;
   const int rank = (int)cluster_rank();
   const int cid = blockIdx.x >> q.log2C, ncl = gridDim.x >> q.log2C;
@@ -956,7 +1024,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
         token = p.tokens[row];
         if (p.weights) weight = p.weights[row];
         if (p.temps) T = p.temps[row];
-        if (q.mode == kModePolicy) {
+        if (is_policy) {
           x0 = p.old_lp[row];
           x1 = p.adv[row];
           if (p.ref_lp) x2 = p.ref_lp[row];
@@ -1025,9 +1093,9 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
         const RowResult r = row_result<ENT>(all, bad ? nan : za, sc);
         RowCoef c{y0, y1};
         PolicyRow o{};
-        if (q.mode == kModePolicy) {
-          o = policy_row(p, r, y0, y1, y2);
-          c = policy_coef(p, o, wt);
+        if (is_policy) {
+          o = policy_row(p, r, y0, y1, y2, wt);
+          c = policy_coef(p, r, o, y0, y1, y2, wt);
         }
         if (GRAD) {
           if (lane == 0) {
@@ -1043,7 +1111,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
           if (p.stats) p.stats[row] = make_float4(r.M, r.l2S, r.l2S_low, r.rest);
           const uint32_t bits = (bad ? kScoreBadToken : 0u) | (r.finite ? 0u : kScoreNonFinite);
           if (bits) atomicOr(p.status, bits);
-          if (q.mode == kModePolicy) policy_add(p, o, r.H, wt, t);
+          if (is_policy) policy_add(p, r, o, y0, y1, y2, wt, t);
         }
         ++count;
       }
@@ -1291,7 +1359,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
   }
   __syncthreads();
   cluster_sync_all();
-  if (q.mode == kModePolicy && rank == 0) {
+  if (is_policy && rank == 0) {
     // a cut-short pass gives NaN, not a part of the sums
     if (*(volatile int*)abort_flag)
       for (int k = 0; k < kPolicyTerms; ++k) t[k] = (double)nan;
@@ -1327,6 +1395,7 @@ __global__ void __launch_bounds__(kShortThreads, GRAD ? 6 : 8)
   const int tid = threadIdx.x % kT;  // in the row
   const RowRange range = row_range(p);
   const float nan = __int_as_float(0x7fc00000);
+  const bool is_policy = ENT && mode == kModePolicy;  // always with entropies
   double t[kPolicyTerms] = {};
   int flip = 0;
   // W = 4: the block's warps share a row and meet at barriers
@@ -1396,7 +1465,7 @@ __global__ void __launch_bounds__(kShortThreads, GRAD ? 6 : 8)
     float T = p.temps ? p.temps[row] : p.temp;
     if (!row_temp_ok(T)) T = nan;
     float x0 = 0.f, x1 = 0.f, x2 = 0.f;
-    if (mode == kModePolicy) {
+    if (is_policy) {
       x0 = p.old_lp[row];
       x1 = p.adv[row];
       if (p.ref_lp) x2 = p.ref_lp[row];
@@ -1441,10 +1510,10 @@ __global__ void __launch_bounds__(kShortThreads, GRAD ? 6 : 8)
     }
     const RowResult r = row_result<ENT>(all, bad ? nan : za, sc);
     RowCoef c{x0, x1};
-    if (mode == kModePolicy) {
-      const PolicyRow o = policy_row(p, r, x0, x1, x2);
-      c = policy_coef(p, o, weight);
-      if (tid == 0) policy_add(p, o, r.H, weight, t);
+    if (is_policy) {
+      const PolicyRow o = policy_row(p, r, x0, x1, x2, weight);
+      c = policy_coef(p, r, o, x0, x1, x2, weight);
+      if (tid == 0) policy_add(p, r, o, x0, x1, x2, weight, t);
     }
     if (tid == 0) {
       if (p.logprobs) p.logprobs[row] = r.lp;
@@ -1471,7 +1540,7 @@ __global__ void __launch_bounds__(kShortThreads, GRAD ? 6 : 8)
       }
     }
   }
-  if (mode == kModePolicy)
+  if (is_policy)
     policy_total<kShortThreads, kRows>(p, tid == 0 ? warp / W : -1, t, blockIdx.x, gridDim.x);
 }
 

@@ -412,7 +412,9 @@ int eb_token_logprobs_backward(eb_scorer_t* h, const eb_score_input_t* in,
      KL = exp(ref - log p_a) - 1 - (ref - log p_a)   (0 without ref_logprobs)
      loss = scale sum_i w (pg + kl_coef KL - entropy_coef H)
    A normalisation (a mean over tokens or sequences) goes into scale and the
-   weights. */
+   weights.  An advantage or coefficient of 0 takes its term out of the loss
+   and the gradient whatever the ratio or the KL beside it (the KL of a banned
+   token is +inf); rows whose ratio or KL is past fp32 are formed in 64 bits. */
 typedef struct {
   const float* old_logprobs; /* [rows] log p_a when the tokens were drawn */
   const float* advantages;   /* [rows] */
