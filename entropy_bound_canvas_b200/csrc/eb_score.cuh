@@ -259,7 +259,8 @@ __device__ __forceinline__ RowRange row_range(const ScoreArgs& p) {
 constexpr float kFarExp = 80.0f, kFarSize = 1e30f;
 
 struct PolicyRow {
-  float pg, kl, dkl;
+  float pg;
+  float gap, back;  // ref - log p_a, e^gap - 1
   bool cut;  // the clipped side is the larger: no gradient through the ratio
   bool far;  // fp32 does not hold it: policy_far does
 };
@@ -279,14 +280,12 @@ __device__ __forceinline__ PolicyRow policy_row(const ScoreArgs& p, const RowRes
   PolicyRow o;
   o.cut = held > free;
   o.pg = o.cut ? held : free;
-  o.kl = o.dkl = 0.f;
+  o.gap = o.back = 0.f;
   float reach = fabsf(x);
   if (p.ref_lp) {
-    const float gap = (ref_lp - r.lp) - r.lp_low;
-    const float back = expm1f(gap);
-    o.kl = back - gap;
-    o.dkl = -back;
-    reach += fabsf(gap);
+    o.gap = (ref_lp - r.lp) - r.lp_low;
+    o.back = expm1f(o.gap);
+    reach += fabsf(o.gap);
   }
   // NaN is far, and so is a w that scale or weight brings past fp32's middle
   const float w = fabsf(weight * (float)p.scale);
@@ -294,6 +293,23 @@ __device__ __forceinline__ PolicyRow policy_row(const ScoreArgs& p, const RowRes
                     w < kFarSize && w > 1.f / kFarSize;
   o.far = !near;
   return o;
+}
+
+// e^x - 1 - x, given e^x - 1.  The difference's relative error grows as
+// 2^-23 / |x| near 0, so there the series x^2 (1/2! + x/3! + ... + x^7/9!): what
+// it leaves out is below 2^-28 of the sum at |x| = 1/2, where the difference
+// loses two bits.
+__device__ __forceinline__ float exp_excess(float x, float back) {
+  if (!(fabsf(x) < 0.5f)) return back - x;
+  float s = 1.f / 362880.f;
+  s = fmaf(s, x, 1.f / 40320.f);
+  s = fmaf(s, x, 1.f / 5040.f);
+  s = fmaf(s, x, 1.f / 720.f);
+  s = fmaf(s, x, 1.f / 120.f);
+  s = fmaf(s, x, 1.f / 24.f);
+  s = fmaf(s, x, 1.f / 6.f);
+  s = fmaf(s, x, 0.5f);
+  return x * x * s;
 }
 
 static __device__ __noinline__ PolicyFar policy_far(float lp, float lp_low, float old_lp,
@@ -326,7 +342,7 @@ __device__ __forceinline__ RowCoef policy_coef(const ScoreArgs& p, const RowResu
   RowCoef c;
   if (!o.far) {
     const float w = weight * (float)p.scale;
-    c.g = w * fmaf(p.kl_coef, o.dkl, o.cut ? 0.f : o.pg);
+    c.g = w * fmaf(p.kl_coef, -o.back, o.cut ? 0.f : o.pg);
     c.h = -w * p.ent_coef;
   } else {
     const PolicyFar f = policy_far(r.lp, r.lp_low, old_lp, adv, ref_lp, p.ref_lp != nullptr,
@@ -345,7 +361,7 @@ __device__ __forceinline__ void policy_add(const ScoreArgs& p, const RowResult& 
                                            float ref_lp, float weight,
                                            double (&t)[kPolicyTerms]) {
   const double w = (double)weight * p.scale;
-  double pg = o.pg, kl = o.kl;
+  double pg = o.pg, kl = exp_excess(o.gap, o.back);
   bool cut = o.cut;
   if (o.far) {
     const PolicyFar f = policy_far(r.lp, r.lp_low, old_lp, adv, ref_lp, p.ref_lp != nullptr,
