@@ -49,14 +49,14 @@ __device__ __forceinline__ float hold_deep(float d) {
 __device__ __forceinline__ bool row_temp_ok(float T) { return T > 0.f && T < INFINITY; }
 // log2(e) / T, rounded once or nearly so, and what that left.
 struct Scale {
-  float c2, low;
+  float c2, low, T;
 };
 __device__ __forceinline__ Scale row_scale(float T) {
   const float r = __frcp_rn(T), q = kLog2e * r;
   // log2(e) is kLog2e in fp32 plus 1.92596e-8
   constexpr float kLog2eLow = 1.925963033500e-8f;
   const float c2 = fmaf(fmaf(-q, T, kLog2e) + kLog2eLow, r, q);
-  return Scale{c2, (fmaf(-c2, T, kLog2e) + kLog2eLow) * r};
+  return Scale{c2, (fmaf(-c2, T, kLog2e) + kLog2eLow) * r, T};
 }
 __device__ __forceinline__ float log2e_over(float T) { return row_scale(T).c2; }
 
@@ -150,6 +150,10 @@ struct RowResult {
   bool finite;
 };
 
+// Beyond 2^24 nats the part of log p_a below fp32 is more than its roundings
+// leave of it, so it is dropped.
+constexpr float kNoLow = 16777216.f;
+
 // s: the sums without the token; za: the token's logit (NaN: a bad token).
 // log2 S is kept as a + b, a an integer or d_a and b small, so that the
 // differences log p_a and H round only their own size.  ENT: Q is there; it
@@ -191,11 +195,15 @@ __device__ __forceinline__ RowResult row_result(RowSums s, float za, Scale sc) {
     constexpr float kLn2Low = -1.904654323148236e-9f;  // ln 2 - kLn2
     r.lp = kLn2 * s2;
     r.lp_low = fmaf(kLn2, s2, -r.lp) + fmaf(kLn2, low, kLn2Low * s2);
-    if (!(r.lp > -INFINITY)) r.lp_low = 0.f;  // a banned token
     const float sum = r.lp + r.lp_low;
     r.lp_low = r.lp_low - (sum - r.lp);
     r.lp = sum;
-    if (!(r.lp > -INFINITY)) r.lp_low = 0.f;
+    if (!(da > -INFINITY) || !(r.lp > -kNoLow)) {
+      r.lp_low = 0.f;
+      // d_a may be past fp32 where log p_a is not, and so may M - z_a
+      if (!(da > -INFINITY))
+        r.lp = !(za > -INFINITY) ? za : gap > -INFINITY ? gap / sc.T : za / sc.T - M / sc.T;
+    }
   }
   r.M = M;
   r.l2S = a + b;
