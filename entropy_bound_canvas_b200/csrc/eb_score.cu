@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -168,8 +169,8 @@ namespace {
 
 size_t elt_bytes(int dtype) { return dtype == EB_F32 ? 4 : 2; }
 
-// Positive and finite, as the fp32 that the kernels use.
-bool temperature_ok(double t) { return (float)t > 0.f && std::isfinite((float)t); }
+// Positive, normal and finite, as the fp32 that the kernels use.
+bool temperature_ok(double t) { return (float)t >= FLT_MIN && std::isfinite((float)t); }
 
 // Sizes, types and pointers every call over logits shares.
 int check_input(const eb_scorer* h, const eb_score_input_t* in) {

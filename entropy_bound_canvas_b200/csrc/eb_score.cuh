@@ -46,7 +46,8 @@ __device__ __forceinline__ float hold_deep(float d) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(d), "f"(-kDeep));
   return r;
 }
-__device__ __forceinline__ bool row_temp_ok(float T) { return T > 0.f && T < INFINITY; }
+// Below fp32's smallest normal number 1/T and log2(e)/T are past its largest.
+__device__ __forceinline__ bool row_temp_ok(float T) { return T >= FLT_MIN && T < INFINITY; }
 // log2(e) / T, rounded once or nearly so, and what that left.
 struct Scale {
   float c2, low, T;

@@ -361,8 +361,9 @@ void eb_sampler_destroy(eb_sampler_t* h);
  *     as 0 and its gradient as zeros.  A token >= V gives NaN results and
  *     sets EB_STATUS_BAD_TOKEN.
  *   - temperatures [rows] fp32 (device), or NULL: `temperature` for every
- *     row (finite, > 0).  A per-row temperature that is not finite and
- *     positive gives NaN results and sets EB_STATUS_NONFINITE.
+ *     row (as fp32 positive, finite and normal, EB_ERR_INVALID_ARG otherwise).
+ *     A per-row temperature that is not gives NaN results and sets
+ *     EB_STATUS_NONFINITE.
  *   - Log-probabilities near 0 (p_a near 1) keep their relative precision.
  *   - d_logits [rows][ldd], the logits' type, each element rounded once;
  *     elements past V of a row are left as they are.  It may be the logits

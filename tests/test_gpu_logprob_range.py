@@ -113,3 +113,27 @@ def test_a_banned_token_among_lowest_values(scorer, V, T):
     assert abs(float(r.entropies[0]) - math.log(V - 1)) < 1e-5
     assert abs(float(r.logprobs[1]) + math.log(V)) < 1e-5
     assert scorer.status() == 0
+
+
+@pytest.mark.parametrize("V", [40, 20000])
+def test_the_smallest_temperatures(E, scorer, V):
+    """fp32's smallest normal number is one; what lies below it (its reciprocal
+    is past fp32) is refused, per row reported."""
+    tiny = torch.finfo(F32).tiny
+    z, tokens, _ = R.make_logits(4, V, F32, 3, DEV)
+    tokens = z.argmax(1).to(torch.int32)
+    zero = torch.zeros(4, device=DEV)
+    r = scorer.token_logprobs(z, tokens, temperature=tiny)
+    assert torch.equal(r.logprobs, zero) and torch.equal(r.entropies, zero)
+    assert (scorer.token_logprobs_backward(z, tokens, zero + 1, temperature=tiny) == 0).all()
+    assert scorer.status() == 0
+    h, w = (torch.zeros((n, 8), dtype=BF16, device=DEV) for n in (4, 9))
+    for T in (tiny / 2, 1e-40, 1e-45):
+        with pytest.raises(E.EBError):
+            scorer.token_logprobs(z, tokens, temperature=T)
+        with pytest.raises(E.EBError):
+            scorer.lmhead_logprobs(h, w, tokens % 9, temperature=T)
+        each = torch.tensor([1.0, T, 1.0, tiny], dtype=F32, device=DEV)
+        r = scorer.token_logprobs(z, tokens, temperature=each)
+        assert torch.equal(torch.isnan(r.logprobs), each < tiny)
+        assert scorer.status(clear=True) == E.STATUS_NONFINITE
