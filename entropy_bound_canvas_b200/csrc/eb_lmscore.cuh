@@ -206,6 +206,7 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kLsThread
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  uint32_t* copied = reinterpret_cast<uint32_t*>(abort_flag + 1);  // stages this CTA has asked for
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = PAIR ? (int)cluster_rank() : 0;
@@ -243,12 +244,31 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kLsThread
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // A wait that gave up cuts the pair short.
   auto fail = [&]() {
     atomicOr(p.status, kScoreTimeout);
     *(volatile int*)abort_flag = 1;
+    if (PAIR) st_cluster(map_rank(smem_u32(abort_flag), rank ^ 1), 1u);
   };
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {  // the whole warp, one outcome
     return (bool)__all_sync(0xffffffffu, lm_wait(bar, parity, p.wait_ns, abort_flag));
+  };
+  // This CTA's copies of stage `kb` of tile `t`, into slot `s`.
+  auto copy_stage = [&](int t, int kb, int s, uint64_t keep, uint64_t wpol) {
+    const int y = (nt_lo + t) * kLsBN + rank * kLsHalf;
+    unsigned char* dst = smem + s * S::kStage;
+    if (PAIR) {
+      // the first CTA's barrier counts both CTAs' bytes
+      const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
+      if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::kStage);
+      tma_load_pair(dst, &tm_h, kb * kLsBK, row0, bar, keep);
+      tma_load_pair(dst + kLsABytes, &tm_w, kb * kLsBK, y, bar, wpol);
+    } else {
+      mbar_arrive_expect_tx(&full[s], S::kStage);
+      tma_load_2d(dst, &tm_h, kb * kLsBK, row0, &full[s], keep);
+      tma_load_2d(dst + kLsABytes, &tm_w, kb * kLsBK, y, &full[s], wpol);
+      tma_load_2d(dst + kLsABytes + kLsBBytes, &tm_w, kb * kLsBK, y + kLsHalf, &full[s], wpol);
+    }
   };
 
   if (warp == 0) {
@@ -258,36 +278,23 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kLsThread
       // W: read once, or by every row tile at about the same time
       const uint64_t wpol = p.rows > S::kBM ? keep : evict_first_policy();
       int s = 0;
-      uint32_t phase = 1u;  // an empty stage's first wait passes at once
+      uint32_t phase = 1u, n = 0;  // an empty stage's first wait passes at once
       bool ok = true;
       for (int t = 0; t < n_tiles && ok; ++t) {
-        const int y = (nt_lo + t) * kLsBN + rank * kLsHalf;
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = 0; kb < KB; ++kb, ++n) {
           if (!lm_wait(&empty[s], phase, p.wait_ns, abort_flag)) {
             fail();
             ok = false;
             break;
           }
-          unsigned char* dst = smem + s * S::kStage;
-          if (PAIR) {
-            // the first CTA's barrier counts both CTAs' bytes
-            const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::kStage);
-            tma_load_pair(dst, &tm_h, kb * kLsBK, row0, bar, keep);
-            tma_load_pair(dst + kLsABytes, &tm_w, kb * kLsBK, y, bar, wpol);
-          } else {
-            mbar_arrive_expect_tx(&full[s], S::kStage);
-            tma_load_2d(dst, &tm_h, kb * kLsBK, row0, &full[s], keep);
-            tma_load_2d(dst + kLsABytes, &tm_w, kb * kLsBK, y, &full[s], wpol);
-            tma_load_2d(dst + kLsABytes + kLsBBytes, &tm_w, kb * kLsBK, y + kLsHalf, &full[s],
-                        wpol);
-          }
+          copy_stage(t, kb, s, keep, wpol);
           if (++s == S::kStages) {
             s = 0;
             phase ^= 1u;
           }
         }
       }
+      *copied = n;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------- MMA issuer
@@ -352,10 +359,8 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kLsThread
         }
       }
       if (!ok && lead) fail();
-      // every MMA issued has completed before TMEM is released
       if (lead) commit(drain);
       __syncwarp();
-      mbar_wait(drain, 0u, kDrainLimitNs);
     }
   } else {
     // --------------------------------------------------------- epilogue
@@ -435,12 +440,32 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kLsThread
   }
   tc_fence_before();
   __syncthreads();
-  // after a cut-short pass copies may still be on their way into either CTA's
-  // memory: they land well within this pause
-  if (*(volatile int*)abort_flag) pause_ns(200000);
+  // Every MMA issued has completed before TMEM is released, and the commits'
+  // arrivals, which go to both CTAs, have come before either leaves.
+  if (warp == 1) mbar_wait(drain, 0u, kDrainLimitNs);
   __syncwarp();
   cluster_sync_all();
   tc_fence_after();
+  // After a pass cut short copies may still be on their way into either CTA's
+  // memory.  Nobody copies or reads stages any more, so each CTA asks for those
+  // that only the other one has asked for (at most a ring of them); then every
+  // phase of the barriers has both CTAs' bytes to come, and is waited for.
+  if (*(volatile int*)abort_flag) {
+    if (warp == 0 && lane == 0) {
+      const uint32_t mine = *copied;
+      const uint32_t other = PAIR ? ld_cluster(map_rank(smem_u32(copied), rank ^ 1)) : mine;
+      const uint32_t n = max(mine, other);
+      const uint64_t once = evict_first_policy();
+      for (uint32_t i = mine; i < n; ++i)
+        copy_stage(i / KB, i % KB, i % S::kStages, once, once);
+      if (rank == 0)
+        for (uint32_t i = n > S::kStages ? n - S::kStages : 0; i < n; ++i)
+          mbar_wait(&full[i % S::kStages], (i / S::kStages) & 1u, kDrainLimitNs);
+    }
+    __syncwarp();
+    __syncthreads();
+    cluster_sync_all();
+  }
   if (warp == 0) {
     __syncwarp();
     if (PAIR) {

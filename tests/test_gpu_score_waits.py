@@ -66,3 +66,34 @@ def test_every_call_reports_a_short_limit(E, dtype, rows, V):
             assert sc.status() == 0, (name, limit)
             assert all(a is None or torch.equal(a, b) for a, b in zip(again, want)), name
     sc.close()
+
+
+@pytest.mark.parametrize("rows,V,d", [(20, 5000, 256), (60, 5000, 2560), (100, 5000, 256),
+                                      (256, 5000, 256), (256, 40001, 2560), (300, 9000, 1000),
+                                      (1300, 20000, 256), (2048, 9001, 2560), (19100, 300, 64)])
+def test_scores_from_hidden_states_report_a_short_limit(E, rows, V, d):
+    """Every form of the product, the CTA pairs among them, cut short at its
+    first wait and later: a wait that ran out is reported, rows are right or NaN,
+    and the next call is right at once."""
+    sc = E.EBScorer(rows, device=DEV)
+    g = torch.Generator().manual_seed(rows)
+    h = torch.randn((rows, d), generator=g).to(BF16).to(DEV)
+    w = torch.randn((V, d), generator=g).to(BF16).to(DEV)
+    tokens = torch.randint(0, V, (rows,), generator=g).to(torch.int32).to(DEV)
+    want = sc.lmhead_logprobs(h, w, tokens)
+    assert sc.status() == 0
+    for limit in (1, 100, 400, 700, 1000, 2000, 4000, 10000) * 3:
+        sc.set_wait_limit(limit)
+        got = sc.lmhead_logprobs(h, w, tokens)
+        bits = sc.status(clear=True)
+        sc.set_wait_limit(0)
+        again = sc.lmhead_logprobs(h, w, tokens)
+        assert bits & E.STATUS_TIMEOUT or limit > 100, limit
+        for a, b, c in zip(got, want, again):
+            assert ((a == b) | torch.isnan(a)).all(), limit
+            # (a warp of padding rows may give up alone)
+            assert bits & E.STATUS_TIMEOUT or not torch.isnan(a).any(), limit
+            assert torch.isnan(a).any() or limit > 100, limit
+            assert torch.equal(b, c), limit
+        assert sc.status() == 0
+    sc.close()
