@@ -521,7 +521,7 @@ struct RingWalk {
 constexpr int kSlots = 4;  // rows between a slot's uses, see the kernel
 
 struct RingLayout {
-  uint32_t part, grad, bars, flag, count, list, total;
+  uint32_t part, grad, bars, flag, count, sent, list, total;
 };
 __host__ __device__ constexpr RingLayout ring_layout() {
   RingLayout y{};
@@ -530,7 +530,8 @@ __host__ __device__ constexpr RingLayout ring_layout() {
   y.bars = y.grad + kSlots * 32u;
   y.flag = y.bars + (2u * (uint32_t)kRingStages + 2u * kSlots) * 8u;
   y.count = y.flag + 16u;
-  y.list = y.count + 16u * 4u;
+  y.sent = y.count + 16u * 4u;
+  y.list = y.sent + 16u * 4u;
   y.total = y.list + (uint32_t)kListRows * 4u;
   return y;
 }
@@ -599,11 +600,6 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.relaxed.cluster.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
-}
-// At least this long.
-__device__ __forceinline__ void pause_ns(uint64_t ns) {
-  const uint64_t t0 = global_ns();
-  while (global_ns() - t0 < ns) __nanosleep(1000);
 }
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -895,6 +891,38 @@ __device__ __forceinline__ int list_rows(const ScoreArgs& p, const RingArgs& q,
   return mine + (p.rows - live - back + ncl - 1) / ncl;
 }
 
+// A finisher's warp waits for every sum still on its way into this CTA, when
+// nobody sends any more.  sent: rows sent by each of this CTA's consumers, rows
+// finished (the next one's sums are awaited), whether the finisher gave up.  A
+// row is sent only after the one kSlots before it was finished everywhere, so at
+// most kSlots rows are in question; of a row of which some sums come, or which
+// is awaited, the warp sends itself those that will not.
+static __device__ __noinline__ void drain_sums(float4* part, uint64_t* sums_in, uint32_t* sent,
+                                               int C) {
+  constexpr int NW = kRingWarps;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank(), done = sent[NW];
+  for (uint32_t k = done; k < done + kSlots; ++k) {
+    const uint32_t par = k % kSlots;
+    unsigned come = 0u;
+    for (int j = 0; j < kMaxCluster * NW / 32; ++j) {
+      const int e = lane + 32 * j;
+      if (e < C * NW && ld_cluster(map_rank(smem_u32(sent + e % NW), e / NW)) > k) come |= 1u << j;
+    }
+    if (k > done && !__any_sync(0xffffffffu, come != 0u)) break;
+    if (k > done && lane == 0) mbar_arrive_expect_tx(&sums_in[par], (uint32_t)(C * NW * 16));
+    __syncwarp();
+    for (int j = 0; j < kMaxCluster * NW / 32; ++j) {
+      const int e = lane + 32 * j;
+      if (e < C * NW && !(come >> j & 1u))
+        st_async4(map_rank(smem_u32(part + par * kMaxCluster * NW + e), rank), 0.f, 0.f, 0.f, 0.f,
+                  map_rank(smem_u32(&sums_in[par]), rank));
+    }
+    mbar_wait(&sums_in[par], (k / kSlots) & 1u, kDrainLimitNs);
+    __syncwarp();
+  }
+}
+
 template <int DT, bool ENT, bool GRAD>
 __global__ void __launch_bounds__(kRingThreads, kRingCtas)
     score_ring_kernel(const ScoreArgs p, const RingArgs q) {
@@ -912,6 +940,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
   uint64_t* result = sums_in + kSlots;   // [kSlots] its factors are there (no gradient: its sums are read)
   int* abort_flag = reinterpret_cast<int*>(ring + lay.flag);
   int* list = reinterpret_cast<int*>(ring + lay.list);
+  uint32_t* sent = reinterpret_cast<uint32_t*>(ring + lay.sent);  // see drain_sums
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool is_policy = ENT && q.mode == kModePolicy;  // always with entropies
@@ -928,6 +957,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
       mbar_init(&result[s], 1);
     }
     *abort_flag = 0;
+    sent[NW + 1] = 0u;
     fence_mbar_init();
   }
   const RowRange range = row_range(p);
@@ -939,9 +969,11 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
     return !q.listed ? min(p.rows, cid + k * ncl) : k < n_rows ? list[k] : p.rows;
   };
 
+  // A wait that gave up cuts the cluster short.
   auto fail = [&]() {
     atomicOr(p.status, kScoreTimeout);
-    *(volatile int*)abort_flag = 1;
+#pragma unroll 1
+    for (int c = 0; c < C; ++c) st_cluster(map_rank(smem_u32(abort_flag), c), 1u);
   };
   // A barrier's phase has completed: one test and a vote, the bounded wait
   // only where that fails.  The outcome is the whole warp's.  The test may
@@ -1151,7 +1183,11 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
       }
       if (!ok) {
         // the rows left, this one first: NaN, not what was there before
-        if (lane == 0) fail();
+        if (lane == 0) {
+          sent[NW] = count;
+          sent[NW + 1] = 1u;
+          fail();
+        }
         for (int k = i - 1 + lane; first && row_at(k) < p.rows; k += 32) {
           const int row = row_at(k);
           if (p.logprobs) p.logprobs[row] = nan;
@@ -1165,6 +1201,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
     RingWalk walk{0, 1, 0u};
     int held = 0;        // ahead: the first slot still held
     uint32_t count = 0;  // rows folded
+    if (lane == 0) sent[warp] = 0u;
     // A folded row whose gradient is still to be written.
     struct Pending {
       int row, token;
@@ -1361,6 +1398,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
         st_async4(map_rank(to, lane), rs.m, rs.R, rs.Q, za,
                   map_rank(smem_u32(&sums_in[par]), lane));
       }
+      if (lane == 0) sent[warp] = count + 1u;
       if (GRAD) {
         const Pending now{row, a, c2, i - 1};
         if (!q.ahead)
@@ -1375,9 +1413,6 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
     if (GRAD && ok && q.ahead && last.row >= 0) write_grad(last, count - 1u);
     if (!ok) {
       if (lane == 0) fail();
-      // sums of this row may still be on their way to other CTAs: they land
-      // well within this pause, before the barrier lets any CTA leave
-      pause_ns(100000);
       // this warp's first granule of each row whose gradient it has not finished: NaN
       for (int k = q.ahead && last.row >= 0 ? last.k : i - 1;
            GRAD && lane == 0 && row_at(k) < p.rows; ++k) {
@@ -1393,6 +1428,12 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
   }
   __syncthreads();
   cluster_sync_all();
+  // after a pass cut short sums may still be on their way
+  if (*(volatile int*)abort_flag) {
+    if (warp == NW + 1 && sent[NW + 1]) drain_sums(part, sums_in, sent, C);
+    __syncthreads();
+    cluster_sync_all();
+  }
   if (is_policy && rank == 0) {
     // a cut-short pass gives NaN, not a part of the sums
     if (*(volatile int*)abort_flag)

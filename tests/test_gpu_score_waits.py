@@ -97,3 +97,38 @@ def test_scores_from_hidden_states_report_a_short_limit(E, rows, V, d):
             assert torch.equal(b, c), limit
         assert sc.status() == 0
     sc.close()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,V", [(600, 9001), (700, 20000), (300, 262144), (2, 1000003)])
+def test_rows_cut_short_on_their_way(E, dtype, rows, V):
+    """Limits that some rows keep and some do not, again and again: rows are
+    right or NaN, a NaN was reported, and the next call is right at once."""
+    sc = E.EBScorer(rows, device=DEV)
+    z, tokens, _ = R.make_logits(rows, V, dtype, 9, DEV)
+    g = torch.ones(rows, device=DEV)
+    out = torch.empty_like(z, memory_format=torch.contiguous_format)
+
+    def calls():
+        yield lambda: sc.token_logprobs(z, tokens)
+        yield lambda: [sc.token_logprobs_backward(z, tokens, g, g, out=out)]
+        yield lambda: [sc.token_logprobs_backward(z, tokens, g, out=out)]
+
+    for call in calls():
+        want = [t.clone() for t in call()]
+        assert sc.status() == 0
+        for limit in (500, 1000, 1500, 2500, 4000, 6000, 9000, 14000, 19000) * 2:
+            out.fill_(7.0)
+            sc.set_wait_limit(limit)
+            got = [t.clone() for t in call()]
+            bits = sc.status(clear=True)
+            sc.set_wait_limit(0)
+            again = call()
+            assert sc.status() == 0
+            for a, b, c in zip(got, want, again):
+                a, b = a.view(rows, -1), b.view(rows, -1)
+                nan = torch.isnan(a).any(1)
+                assert torch.equal(a[~nan], b[~nan]), limit
+                assert bits & E.STATUS_TIMEOUT or not nan.any(), limit
+                assert torch.equal(b, c.view(rows, -1)), limit
+    sc.close()
