@@ -284,8 +284,7 @@ __device__ __forceinline__ PolicyRow policy_row(const ScoreArgs& p, const RowRes
   const float x = (r.lp - old_lp) + r.lp_low;
   const float ratio = expf(x);
   const float free = -adv * ratio;
-  const float held_ratio = ratio < p.clip_lo ? p.clip_lo : ratio > p.clip_hi ? p.clip_hi : ratio;
-  const float held = -adv * held_ratio;
+  const float held = -adv * fminf(fmaxf(ratio, p.clip_lo), p.clip_hi);
   PolicyRow o;
   o.cut = held > free;
   o.pg = o.cut ? held : free;
