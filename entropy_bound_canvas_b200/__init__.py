@@ -510,7 +510,8 @@ class EBScorer:
     one per row.  Results are allocated here unless ``out`` gives the
     gradient's buffer, which may be the logits themselves.  Calls run on the
     device's current stream, never synchronise, and can be captured in a CUDA
-    graph; one scorer per stream at a time.
+    graph (keep the scorer as long as its graphs); one scorer per stream at a
+    time.
     """
 
     def __init__(self, max_rows: int, device=None):

@@ -33,11 +33,12 @@
 // lmscore_finish_kernel.
 //
 // What bounds them, at 262144 ids and d = 2560: up to 64 rows the reading of W
-// (24 rows 213 us, 6.3 TB/s, 0.96 of the measured copy rate).  Above that the
-// tensor cores (85 % busy at 512 rows), and under a steady load the chip's
-// power: 256 rows 338 us (277 in a short burst, at 1.24 PFLOP/s), 2048 rows
-// 2.05 ms (1.34 PFLOP/s, 0.96 of what a library product sustains).  W asked for
-// in L2 some stages ahead: 5 to 15 % slower.
+// (24 rows 208 us, 6.5 TB/s, 0.98 of the measured copy rate).  Above that the
+// tensor cores (84 % busy at 512 rows), and under a steady load the chip's
+// power: 256 rows 356 us (273 in a short burst, at 1.26 PFLOP/s; 234 of zeros,
+// close to the reading of W), 2048 rows 2.11 ms (1.30 PFLOP/s, 0.93 of what a
+// library product sustains; a library product of the same sizes, which writes
+// the logits, 2.10).  W asked for in L2 some stages ahead: 5 to 15 % slower.
 #pragma once
 
 #include "eb_score.cuh"

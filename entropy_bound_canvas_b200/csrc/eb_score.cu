@@ -224,9 +224,9 @@ int share_stages(int64_t row_bytes, int log2C) {
 // its SM, and with every SM holding two; the other constants were fitted to
 // 22 shapes of 100 to 2048 rows on one to eight CTAs each, where the size
 // taken is within 2 % of the best on average and 8 % at most.  262144 bf16:
-// one row, forward, 22.6 us on one CTA and 5.5 on 16; 2048 rows with their
-// gradient 478 us on one CTA each, 400 on two, 436 on four, 528 on eight;
-// 2048 rows of 16000: 46 on one, 55 on two.
+// one row, forward, 22.6 us on one CTA and 5.5 on 16; a policy step of 2048 rows
+// 489 us on one CTA each, 411 on two, 438 on four, 534 on eight; of 2048 rows of
+// 16000, 52 on one, 61 on two, 80 on four.
 int ring_log2C(const eb_scorer* h, int variant, bool f32, bool grad, int64_t rows,
                int64_t row_bytes, double& best_t) {
   const double alone = (grad ? 12.0 : 26.0) * (f32 ? 1.4 : 1.0);
@@ -294,9 +294,9 @@ int launch_rows(const eb_scorer* h, const ScoreArgs& a, int dtype, int mode, boo
   q.log2C = c;
   q.ahead = 2 * share_stages(row_bytes, c) <= kRingStages;
   // Rows shared out by lists: where a cluster takes more than two, and the launch
-  // is long enough for the counting (2048 rows of 262144 bf16 with gradient:
-  // none ignored 416 us against 410, 128 scattered ones 396 against 413, 512
-  // 352 against 390; 1000 rows, scores, none ignored: 96.6 against 93.8).
+  // is long enough for the counting (a policy step of 2048 rows of 262144 bf16:
+  // none ignored 413 us against 408, 128 scattered ones 393 against 402, 512
+  // 351 against 396; 1000 rows, scores, none ignored: 104 against 101).
   const int clusters = std::max(1, std::min(a.rows, most));
   q.listed = a.rows > 2 * clusters && us > kListUs && a.rows <= (kListRows - 2) * clusters;
   cudaLaunchConfig_t lc;
@@ -539,9 +539,14 @@ int eb_lmhead_logprobs(eb_scorer_t* h, const void* hidden, const void* weight, i
   p.logprobs = logprobs;
   p.entropies = entropies;
   // An odd number of 128-row tiles leaves half of the last pair's work padding;
-  // single CTAs take longer for the same tiles, so they win up to 9 tiles (262144
-  // ids, d = 2560: 300 rows 489 us against 539 on pairs, 1100 rows 1303 against
-  // 1331, 1400 rows 1695 against 1570).
+  // single CTAs take longer for the same tiles, so they win up to 9 tiles.  Single
+  // CTAs against pairs, us:
+  //   ids, d           100 rows  300        600        1100         1400
+  //   32003, 256       17 / 18   21 / 23    26 / 29    34 / 37      39 / 41
+  //   32003, 2560      39 / 48   70 / 76    101 / 107  163 / 167    204 / 199
+  //   131072, 1024     60 / 69   105 / 115  152 / 162  275 / 281    344 / 324
+  //   262144, 2560     220 / 264 484 / 568  808 / 825  1358 / 1330  1678 / 1575
+  // (2000 ids, where one launch's latency is most of it: within 2 us.)
   const int tiles = (rows + ebk::kLsRows - 1) / ebk::kLsRows;
   const bool few = rows <= ebk::kLfRows, pair = tiles % 2 == 0 || tiles > 9;
   if (few) {

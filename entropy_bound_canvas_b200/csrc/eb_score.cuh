@@ -465,10 +465,12 @@ __device__ __forceinline__ void policy_total(const ScoreArgs& p, int leader,
 // that are not the row's, and stored element by element.
 //
 // What bounds it: HBM, and close behind it the exponentials and the issue
-// slots.  2048 rows of 262144 bf16: 179 us without a gradient (6.0 TB/s, 0.91
+// slots.  2048 rows of 262144 bf16: 178 us without a gradient (6.0 TB/s, 0.92
 // of the measured copy rate; the exponential unit 60 % and the issue slots
-// 57 % busy), 400 us with the policy loss's (5.4 TB/s counting one read and
-// one write, 0.82; an earlier form's copies and stores alone took 359).
+// 57 % busy), 412 us with the policy loss's (5.2 TB/s counting one read and
+// one write, 0.79; an earlier form's copies and stores alone took 359).  Kept
+// up for seconds, the chip's power limit holds the SM clock at 1.76 GHz: 203
+// and 445 us.
 // One canvas of 256 rows, 31 and 66 us, has two waves of clusters of which
 // the second is three quarters full, and the pipeline to fill and drain.
 // Measured against: 8 KB and 32 KB stages, 6, 10 or 12 consumer warps, three
@@ -1448,7 +1450,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
 // one read to the gradient's write.  A short row's cost is its latency (load,
 // sums, logarithms, store), so what counts is how many are in flight: W = 1
 // up to 4 KB, W = 4 up to 16 KB, four warps to a block, six to eight blocks to
-// an SM.  A policy step: 16 rows of 1024 fp32 4.7 us (one row's latency), 16384
+// an SM.  A policy step: 16 rows of 1024 fp32 5.0 us (one row's latency), 16384
 // rows of 4096 bf16 107 us (2.5 TB/s; the issue slots, 62 % busy, go half to
 // the row's logarithms and loss terms, which each of its warps computes so
 // that no second barrier waits for them).

@@ -350,11 +350,14 @@ void eb_sampler_destroy(eb_sampler_t* h);
  *   - A scorer handle owns a workspace for up to max_rows rows; one handle per
  *     stream at a time (two graphs captured with one handle must not run at
  *     the same time).  Calls allocate nothing, never synchronise and can be
- *     captured in a CUDA graph.
+ *     captured in a CUDA graph, which uses the workspace at every replay: the
+ *     handle is kept as long as its graphs.
  *   - logits [rows][ld] fp32 or bf16, row i at element i ld, ld >= V; any
  *     alignment to the element (rows aligned to 16 bytes load faster).
  *     Logits may be -inf (probability 0); NaN, +inf or a row of only -inf
- *     gives NaN results and sets EB_STATUS_NONFINITE.
+ *     gives NaN results and sets EB_STATUS_NONFINITE.  Probabilities below
+ *     2^-126 of the row's largest count as 0 beside the others' (a token's own
+ *     log-probability is given as far out as fp32 holds it).
  *   - tokens [rows] int32.  A negative token, a policy weight of 0 or (in
  *     eb_preference_loss) a place outside the sequences makes a row ignored:
  *     its logits are not read, its log-probability and entropy are written
@@ -469,7 +472,7 @@ int eb_preference_loss(eb_scorer_t* h, const eb_score_input_t* in,
    scoring under a policy or a reference model.
      hidden [rows][d] bf16, weight [V][d] bf16, device memory, 16-byte
      aligned, row-major, read only; d a multiple of 8 (EB_ERR_UNSUPPORTED
-     otherwise), any V >= 1, rows up to max_rows; an ignored row still takes
+     otherwise) and at most 2^20, V 1 .. 2^30, rows up to max_rows; an ignored row still takes
      part in the product. */
 int eb_lmhead_logprobs(eb_scorer_t* h, const void* hidden, const void* weight, int32_t rows,
                        int32_t V, int32_t d, const int32_t* tokens, const float* temperatures,
