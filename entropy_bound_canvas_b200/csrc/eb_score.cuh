@@ -943,6 +943,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
   int* list = reinterpret_cast<int*>(ring + lay.list);
   uint32_t* sent = reinterpret_cast<uint32_t*>(ring + lay.sent);  // see drain_sums
 
+  uint64_t begun = p.wait_ns < kSuspendHintNs ? global_ns() : 0;  // see wait_limited
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool is_policy = ENT && q.mode == kModePolicy;  // always with entropies
   const int C = 1 << q.log2C;
@@ -984,13 +985,17 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
     return (bool)__all_sync(0xffffffffu, mbar_wait_timed(bar, ph, p.wait_ns, abort_flag));
   };
   // The same, but a limit shorter than that is kept: the finisher's wait for a
-  // row's sums, which are never there at its first test, so that a short limit
-  // runs out in every call.  In every wait the look at the limit costs up to
-  // 3 % (2048 rows of 262144 bf16, scores: 194.6 us against 188.4), in this one
-  // nothing (188.4).
+  // row's sums, counted from the last one's end (the first one's from the
+  // kernel's start, so that sums which are there before the finisher is have
+  // taken their time too): a short limit runs out in every call.  In every wait
+  // the look at the limit costs up to 3 % (2048 rows of 262144 bf16, scores:
+  // 194.6 us against 188.4), in this one nothing (188.4).
   auto wait_limited = [&](uint64_t* bar, uint32_t ph) {
     if (p.wait_ns >= kSuspendHintNs) return wait(bar, ph);
-    return (bool)__all_sync(0xffffffffu, mbar_wait_timed(bar, ph, p.wait_ns, abort_flag));
+    const bool came = mbar_wait_timed(bar, ph, p.wait_ns, abort_flag) &&
+                      global_ns() - begun <= p.wait_ns;
+    begun = global_ns();
+    return (bool)__all_sync(0xffffffffu, came);
   };
   bool ok = true;
   const float nan = __int_as_float(0x7fc00000);

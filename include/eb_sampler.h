@@ -485,8 +485,8 @@ int eb_scorer_status(eb_scorer_t* h, uint32_t* status, int clear, void* stream);
 /* Diagnostic hook: the limit, in nanoseconds, of the scorer's internal waits
    (0 = the default of 2 s).  A wait that runs out sets EB_STATUS_TIMEOUT; the
    call's results are then NaN or unwritten, and the device stays usable.
-   Below 20 us the limit is kept where a row's sums are awaited and in the
-   LM-head kernels, so that a tiny limit runs out in every call on logits of
+   Below 20 us the limit is kept where a row's sums are awaited (counted from the
+   last row's end, or the kernel's start) and in the LM-head kernels, so that a tiny limit runs out in every call on logits of
    more than 16 KB a row or on hidden states; the other waits of the rows'
    kernel may be suspended until what they wait for has come. */
 int eb_scorer_set_wait_limit(eb_scorer_t* h, uint64_t limit_ns);

@@ -132,3 +132,21 @@ def test_rows_cut_short_on_their_way(E, dtype, rows, V):
                 assert bits & E.STATUS_TIMEOUT or not nan.any(), limit
                 assert torch.equal(b, c.view(rows, -1)), limit
     sc.close()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("limit", [1, 100])
+def test_a_single_row_reports_a_short_limit_every_time(E, dtype, limit):
+    """One row has one wait for its sums: it runs out also where its warp comes to
+    it late and finds them there."""
+    sc = E.EBScorer(4, device=DEV)
+    z, tokens, _ = R.make_logits(1, 20001, dtype, 9, DEV)
+    want = sc.token_logprobs(z, tokens)
+    sc.set_wait_limit(limit)
+    for i in range(300):
+        r = sc.token_logprobs(z, tokens, entropies=i % 2 == 0)
+        assert sc.status(clear=True) & E.STATUS_TIMEOUT, i
+        assert torch.isnan(r.logprobs).all(), i
+    sc.set_wait_limit(0)
+    assert torch.equal(sc.token_logprobs(z, tokens).logprobs, want.logprobs)
+    sc.close()
